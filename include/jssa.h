@@ -97,7 +97,11 @@ enum jssa_fn {
   JSSA_FN_COMPUTE_BASIS = 5,
   JSSA_FN_MLA_ATTEND = 6,
   JSSA_FN_MLA_DECODE = 7,
-  JSSA_FN_DECODE_HOST = 8
+  JSSA_FN_DECODE_HOST = 8,
+  JSSA_FN_DENSE_DECODE_MASS = 9,
+  JSSA_FN_INDEXED_ATTEND_MASS = 10,
+  JSSA_FN_DECODE_MASS = 11,
+  JSSA_FN_TREE_ATTEND = 12
 };
 
 /* Text for a status code (static storage). */
@@ -122,13 +126,15 @@ JSSA_API long long jssa_set_wait_limit(long long cycles);
  * Bytes of device workspace the entry point `fn` needs for these sizes (written to *bytes; 0
  * means none). max_pages and page_size are the block-table width and page size the call will
  * get (every seq_len is at most max_pages*page_size); budget is the token budget B, except for
- * JSSA_FN_DENSE_DECODE where it carries the call's window (<= 0: full context); the basis
+ * JSSA_FN_DENSE_DECODE and JSSA_FN_DENSE_DECODE_MASS where it carries the call's window (<= 0:
+ * full context) and JSSA_FN_TREE_ATTEND where it carries the nodes per sequence; the basis
  * ignores it. Score + top-B keeps its candidate keys and positions in the workspace. The
  * split-K attention entry points keep a per-(sequence, KV head) ticket counter at the start of
  * theirs: for jssa_indexed_attend and jssa_dense_decode those counters must be zero when the call
  * starts -- clear the workspace with jssa_workspace_init before its first use and again after it
  * served another entry point or a larger batch*h_kv (the kernels leave the counters at zero on
- * exit). jssa_decode clears its counters itself. Calls that share one workspace must not overlap
+ * exit). jssa_decode clears its counters itself; the mass forms and jssa_tree_attend keep none
+ * (their workspace needs no clearing). Calls that share one workspace must not overlap
  * on the GPU.
  */
 JSSA_API int jssa_workspace_size(int fn, int batch, int h_q, int h_kv, int d, int max_pages,
@@ -393,6 +399,119 @@ JSSA_API int jssa_decode_host(const jssa_bf16* q_host, const jssa_bf16* k_new_ho
  * then on its `stream`. No-op for a workspace that has not been used by jssa_decode_host.
  */
 JSSA_API int jssa_decode_host_join(const void* ws, jssa_stream_t stream);
+
+/*
+ * Attention mass: the attention calls below also add every attended position's weight to a running
+ * sum, from which jssa_evict chooses what the cache keeps. The pages have no counterpart to this or
+ * to the other cache-maintenance calls (tree attention, commit, eviction).
+ *   mass[b, h, t] += sum over the G query heads i of KV head h of softmax_i(t)
+ * for every attended position t; other entries are not touched. mass: float32, row (b, h) at
+ * mass + (b*h_kv + h)*mass_stride, mass_stride >= max_pages*page_size (JSSA_ERR_SHAPE otherwise).
+ * Scores and sums are fp32. All other arguments, the output and the errors as in the call without
+ * mass (jssa_dense_decode, jssa_indexed_attend, jssa_decode). An index set that names a position
+ * twice is not allowed (its sum would be undefined). ws: >= jssa_workspace_size of
+ * JSSA_FN_DENSE_DECODE_MASS, JSSA_FN_INDEXED_ATTEND_MASS or JSSA_FN_DECODE_MASS, 16-byte aligned:
+ * partial outputs and h_q*4 bytes of scores per attended position; no clearing needed.
+ */
+JSSA_API int jssa_dense_decode_mass(const jssa_bf16* q, const jssa_bf16* k_cache,
+                                    const jssa_bf16* v_cache, int64_t kv_page_stride,
+                                    int64_t kv_slot_stride, int64_t kv_head_stride,
+                                    const int32_t* block_table, int max_pages,
+                                    const int32_t* seq_lens, int batch, int h_q, int h_kv, int d,
+                                    int64_t num_pages, int page_size, int window,
+                                    float softmax_scale, float* mass, int64_t mass_stride,
+                                    jssa_bf16* out, void* ws, size_t ws_bytes,
+                                    jssa_stream_t stream);
+JSSA_API int jssa_indexed_attend_mass(const jssa_bf16* q, const jssa_bf16* k_cache,
+                                      const jssa_bf16* v_cache, int64_t kv_page_stride,
+                                      int64_t kv_slot_stride, int64_t kv_head_stride,
+                                      const int32_t* block_table, int max_pages, const int32_t* idx,
+                                      const int32_t* count, int batch, int h_q, int h_kv, int d,
+                                      int budget, int64_t num_pages, int page_size,
+                                      float softmax_scale, float* mass, int64_t mass_stride,
+                                      jssa_bf16* out, void* ws, size_t ws_bytes,
+                                      jssa_stream_t stream);
+JSSA_API int jssa_decode_mass(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_new,
+                              jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                              int64_t kv_slot_stride, int64_t kv_head_stride, uint8_t* score_cache,
+                              const float* basis, const int32_t* block_table, int max_pages,
+                              const int32_t* seq_lens, int batch, int h_q, int h_kv, int d, int r,
+                              int64_t num_pages, int page_size, int budget, float softmax_scale,
+                              float* mass, int64_t mass_stride, int32_t* idx, int32_t* count,
+                              jssa_bf16* out, void* ws, size_t ws_bytes, jssa_stream_t stream);
+
+/*
+ * Eviction by accumulated attention mass. For every sequence b and KV head h the kept set is the
+ * last `recent` positions and, of the positions before them, the keep - recent with the largest
+ * mass (ties to the lower position, every NaN counts as the largest value); all positions when
+ * seq_len <= keep. idx int32 [batch, h_kv, keep]: the kept positions, ascending, padded with -1;
+ * count int32 [batch, h_kv] = min(keep, seq_len); lens_out int32 [batch] = min(keep, seq_len).
+ * The rows of the kept positions then move to positions 0, 1, ... of dst_block_table, in order:
+ * row idx[b, h, i] becomes row i of K, V, the scoring cache (when non-NULL) and mass_out;
+ * mass_out[b, h, t] becomes 0 for count <= t < seq_len. Rows of a KV head move independently of the
+ * other heads', as the selections are; keys are moved as they are (rotary phases keep the original
+ * positions). Nothing else is written.
+ * dst_block_table, int32 [batch, dst_max_pages]: block_table itself moves the rows in place; any
+ * other table must name pages that this call reads for no sequence (for instance when the source
+ * pages are shared). mass_out may be mass. Positions of dst_block_table beyond its end or its
+ * unusable pages are skipped and flagged, as are unusable source pages (the destination row is left
+ * as it was). 1 <= keep, 0 <= recent <= keep; lens_out must not be seq_lens, nor idx, count and
+ * lens_out overlap an input. score_bytes: bytes of one scoring row (16, 32 or 64: r, or 2 r for a
+ * bf16 scoring cache), the scoring cache as in the conventions. mass, mass_out: float32, rows of
+ * mass_stride elements as in jssa_dense_decode_mass. No workspace.
+ */
+JSSA_API int jssa_evict(const float* mass, int64_t mass_stride, jssa_bf16* k_cache,
+                        jssa_bf16* v_cache, int64_t kv_page_stride, int64_t kv_slot_stride,
+                        int64_t kv_head_stride, uint8_t* score_cache, int score_bytes,
+                        const int32_t* block_table, int max_pages, const int32_t* dst_block_table,
+                        int dst_max_pages, const int32_t* seq_lens, int batch, int h_kv, int d,
+                        int64_t num_pages, int page_size, int keep, int recent, int32_t* idx,
+                        int32_t* count, float* mass_out, int32_t* lens_out, jssa_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache. seq_lens[b] counts the committed
+ * tokens (the context); node i of sequence b is a token whose K / V row is at position
+ * seq_lens[b] + i. parents int32 [batch, n_nodes]: -1 = the node follows the last committed token,
+ * 0 <= p < i = it follows node p, below -1 = unused (padding: its output rows are zero, its cache
+ * row is neither read nor written). A parent >= i, or one that names an unused node, makes the node
+ * unused and raises JSSA_DEVERR_INDEX.
+ *   out[b, i, hq] = softmax(softmax_scale * q[b, i, hq] K^T) V
+ * over the node's context positions, itself and its ancestors. The context is every position below
+ * seq_lens[b]; with window > 0 the positions above seq_len + depth - window, where the node's depth
+ * is the number of its ancestors (ancestors outside the window are left out, too); with idx
+ * non-NULL (window must be <= 0) the positions idx[b, h, 0:count[b, h]] (those of a selection over
+ * the committed tokens; budget is the width of idx, ignored without it).
+ * k_new, v_new: bf16 [batch, n_nodes, h_kv, d] or both NULL: when given, the used nodes' rows are
+ * written into the caches by this call. q, out: bf16 [batch, n_nodes, h_q, d] contiguous, 16-byte
+ * aligned. 0 <= n_nodes <= 64 (JSSA_ERR_UNSUPPORTED beyond). Masked positions contribute nothing,
+ * whatever their rows hold. ws: >= jssa_workspace_size(JSSA_FN_TREE_ATTEND, batch, h_q, h_kv, d,
+ * max_pages, page_size, n_nodes), 16-byte aligned; no clearing needed.
+ */
+JSSA_API int jssa_tree_attend(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_new,
+                              jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                              int64_t kv_slot_stride, int64_t kv_head_stride,
+                              const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                              const int32_t* parents, const int32_t* idx, const int32_t* count,
+                              int batch, int n_nodes, int h_q, int h_kv, int d, int budget,
+                              int64_t num_pages, int page_size, int window, float softmax_scale,
+                              jssa_bf16* out, void* ws, size_t ws_bytes, jssa_stream_t stream);
+
+/*
+ * Commit of the accepted nodes of a drafted tree: for i < n_path[b] the row of position
+ * seq_lens[b] + path[b, i] (K, V and, when score_cache is non-NULL, the scoring row) moves to
+ * position seq_lens[b] + i, for every KV head; lens_out[b] = seq_lens[b] + n_path[b]. path int32
+ * [batch, max_path], max_path <= 64, entries in [0, 64); n_path int32 [batch]. Every row is read
+ * before any is written, so the entries may come in any order. An entry out of range or on an
+ * unusable page is skipped (its destination row is left as it was) and flagged; an n_path outside
+ * [0, max_path], or past the end of the block table, is clamped and flagged. lens_out must not be
+ * seq_lens. score_bytes as in jssa_evict. No workspace.
+ */
+JSSA_API int jssa_tree_commit(jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                              int64_t kv_slot_stride, int64_t kv_head_stride, uint8_t* score_cache,
+                              int score_bytes, const int32_t* block_table, int max_pages,
+                              const int32_t* seq_lens, const int32_t* path, const int32_t* n_path,
+                              int max_path, int batch, int h_kv, int d, int64_t num_pages,
+                              int page_size, int32_t* lens_out, jssa_stream_t stream);
 
 /* Size of the device scratch array used by jssa_indexed_attend_noalloc (per GPU, bytes). */
 #define JSSA_NOALLOC_SCRATCH_BYTES (4u << 20)

@@ -9,15 +9,16 @@ the library is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
 import torch
 
 from . import _lib
-from ._lib import (FN_COMPUTE_BASIS, FN_DECODE, FN_DECODE_HOST, FN_DENSE_DECODE,
-                   FN_INDEXED_ATTEND, FN_MLA_ATTEND, FN_MLA_DECODE, FN_SCORE_TOPK, JSSAError, call,
-                   check, load)
+from ._lib import (FN_COMPUTE_BASIS, FN_DECODE, FN_DECODE_HOST, FN_DECODE_MASS, FN_DENSE_DECODE,
+                   FN_DENSE_DECODE_MASS, FN_INDEXED_ATTEND, FN_INDEXED_ATTEND_MASS, FN_MLA_ATTEND,
+                   FN_MLA_DECODE, FN_SCORE_TOPK, FN_TREE_ATTEND, JSSAError, call, check, load)
 
 __all__ = [
     "gather_kv", "staged_pages", "gather_then_attend", "mla_calibrate_accumulate", "mla_attend",
@@ -25,7 +26,7 @@ __all__ = [
     "JSSAError", "workspace_size", "Workspace", "calibrate_accumulate", "compute_basis",
     "calibrate", "store", "score_topk", "indexed_attend", "dense_decode", "decode",
     "device_error", "kv_strides", "default_rank", "PagedLayer", "HostPipeline", "Calibration", "save_basis",
-    "load_basis", "set_wait_limit",
+    "load_basis", "set_wait_limit", "tree_attend", "tree_commit", "evict", "TREE_MAX_NODES",
 ]
 
 
@@ -96,6 +97,83 @@ def _ws(device: torch.device, ws: Optional[Workspace], fn: int) -> Workspace:
     if key not in _default_ws:
         _default_ws[key] = Workspace(device)
     return _default_ws[key]
+
+
+def _scratch(ws: Optional[Workspace], nbytes: int, device: torch.device):
+    """(pointer, bytes, owner) of a workspace that needs no clearing: the caller's, else memory of
+    this call alone, taken from torch's allocator on the current stream (so calls on other streams
+    and captured graphs never share it)."""
+    if ws is not None:
+        p, n = ws.get(nbytes)
+        return p, n, None
+    if nbytes == 0:
+        return None, 0, None
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return buf.data_ptr(), nbytes, buf
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(fn, batch, h_q, h_kv, d, max_pages, page_size, budget, device_index):
+    return workspace_size(fn, batch, h_q, h_kv, d, max_pages, page_size, budget)
+
+
+def _call_on(device: torch.device, name: str, *args) -> None:
+    """Call an entry point with ``device`` current, on its current stream."""
+    if torch.cuda.current_device() == device.index:
+        call(name, *args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            call(name, *args, _stream(device))
+
+
+def _shape(t: torch.Tensor, name: str, shape, device: torch.device):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _need_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, h_kv=None, d=None):
+    """(strides, num_pages, page_size, h_kv, d) of a K / V cache pair."""
+    _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
+    _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
+    strides = kv_strides(k_cache)
+    if kv_strides(v_cache) != strides or v_cache.shape != k_cache.shape:
+        raise ValueError("K and V caches must share one layout")
+    if v_cache.device != k_cache.device:
+        raise ValueError("K and V caches must be on one device")
+    return (strides, *k_cache.shape)
+
+
+def _need_table(block_table, seq_lens, device, batch=None, name="block_table"):
+    _need(block_table, name, torch.int32)
+    if block_table.dim() != 2 or (batch is not None and block_table.shape[0] != batch):
+        raise ValueError(f"{name} must be [batch, max_pages]")
+    if block_table.device != device:
+        raise ValueError(f"{name} must be on {device}, got {block_table.device}")
+    if seq_lens is not None:
+        _need(seq_lens, "seq_lens", torch.int32)
+        _shape(seq_lens, "seq_lens", (block_table.shape[0],), device)
+
+
+def _need_mass(mass, name, batch, h_kv, capacity, device):
+    _need(mass, name, torch.float32)
+    if mass.dim() != 3 or mass.shape[:2] != (batch, h_kv) or mass.shape[2] < capacity:
+        raise ValueError(f"{name} must be [batch, h_kv, >= max_pages * page_size]")
+    if mass.device != device:
+        raise ValueError(f"{name} must be on {device}, got {mass.device}")
+
+
+def _need_codes(score_cache, num_pages, h_kv, page_size, device):
+    """Bytes of a scoring row (0 without a scoring cache)."""
+    if score_cache is None:
+        return 0
+    bf16 = score_cache.dtype == torch.bfloat16
+    _need(score_cache, "score_cache", torch.bfloat16 if bf16 else torch.uint8)
+    if score_cache.dim() != 4:
+        raise ValueError("score_cache must be [num_pages, h_kv, page_size, r]")
+    _shape(score_cache, "score_cache", (num_pages, h_kv, page_size, score_cache.shape[3]), device)
+    return score_cache.shape[3] * (2 if bf16 else 1)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -332,8 +410,12 @@ def score_topk(q: torch.Tensor, basis: torch.Tensor, score_cache: torch.Tensor,
 def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    block_table: torch.Tensor, idx: torch.Tensor, count: torch.Tensor,
                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                   ws: Optional[Workspace] = None) -> torch.Tensor:
-    """Gather-free attention of every query head over its KV head's index set."""
+                   ws: Optional[Workspace] = None,
+                   mass: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gather-free attention of every query head over its KV head's index set. With ``mass``
+    (float32 ``[batch, h_kv, >= max_pages * page_size]``) every attended position's weight, summed
+    over the KV head's query heads, is added to its entry (an index set then names no position
+    twice)."""
     _need(q, "q", torch.bfloat16)
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
@@ -348,6 +430,19 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     budget = idx.shape[2]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     out = torch.empty_like(q) if out is None else out
+    if mass is not None:
+        _need_table(block_table, None, q.device, batch)
+        _shape(idx, "idx", (batch, h_kv, budget), q.device)
+        _shape(count, "count", (batch, h_kv), q.device)
+        _need_mass(mass, "mass", batch, h_kv, block_table.shape[1] * page_size, q.device)
+        p, n, _hold = _scratch(ws, _ws_bytes(FN_INDEXED_ATTEND_MASS, batch, h_q, h_kv, d,
+                                             block_table.shape[1], page_size, budget,
+                                             q.device.index), q.device)
+        _call_on(q.device, "jssa_indexed_attend_mass", q.data_ptr(), k_cache.data_ptr(),
+                 v_cache.data_ptr(), *strides, block_table.data_ptr(), block_table.shape[1],
+                 idx.data_ptr(), count.data_ptr(), batch, h_q, h_kv, d, budget, num_pages,
+                 page_size, scale, mass.data_ptr(), mass.shape[2], out.data_ptr(), p, n)
+        return out
     w = _ws(q.device, ws, FN_INDEXED_ATTEND)
     p, n = w.get(workspace_size(FN_INDEXED_ATTEND, batch, h_q, h_kv, d, block_table.shape[1],
                                 page_size, budget))
@@ -474,8 +569,10 @@ def gather_then_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
 def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_table: torch.Tensor, seq_lens: torch.Tensor, scale: Optional[float] = None,
                  window: int = -1, out: Optional[torch.Tensor] = None,
-                 ws: Optional[Workspace] = None) -> torch.Tensor:
-    """Dense paged decode attention over ``[max(0, L - window), L)`` (all when window <= 0)."""
+                 ws: Optional[Workspace] = None,
+                 mass: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Dense paged decode attention over ``[max(0, L - window), L)`` (all when window <= 0).
+    ``mass`` as in :func:`indexed_attend`."""
     _need(q, "q", torch.bfloat16)
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
@@ -489,6 +586,16 @@ def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     max_pages = block_table.shape[1]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     out = torch.empty_like(q) if out is None else out
+    if mass is not None:
+        _need_table(block_table, seq_lens, q.device, batch)
+        _need_mass(mass, "mass", batch, h_kv, max_pages * page_size, q.device)
+        p, n, _hold = _scratch(ws, _ws_bytes(FN_DENSE_DECODE_MASS, batch, h_q, h_kv, d, max_pages,
+                                             page_size, window, q.device.index), q.device)
+        _call_on(q.device, "jssa_dense_decode_mass", q.data_ptr(), k_cache.data_ptr(),
+                 v_cache.data_ptr(), *strides, block_table.data_ptr(), max_pages,
+                 seq_lens.data_ptr(), batch, h_q, h_kv, d, num_pages, page_size, window, scale,
+                 mass.data_ptr(), mass.shape[2], out.data_ptr(), p, n)
+        return out
     w = _ws(q.device, ws, FN_DENSE_DECODE)
     p, n = w.get(workspace_size(FN_DENSE_DECODE, batch, h_q, h_kv, d, max_pages, page_size, window))
     call("jssa_dense_decode", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *strides,
@@ -502,9 +609,9 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
            basis: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, budget: int,
            scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
            idx: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None,
-           ws: Optional[Workspace] = None):
+           ws: Optional[Workspace] = None, mass: Optional[torch.Tensor] = None):
     """One JSSA decode step for one layer (store new token, score + top-B, indexed attend).
-    Returns ``(out, idx, count)``."""
+    ``mass`` as in :func:`indexed_attend`. Returns ``(out, idx, count)``."""
     _need(q, "q", torch.bfloat16)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
@@ -528,6 +635,21 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
         idx = torch.empty((batch, h_kv, budget), dtype=torch.int32, device=q.device)
     if count is None:
         count = torch.empty((batch, h_kv), dtype=torch.int32, device=q.device)
+    if mass is not None:
+        _need_table(block_table, seq_lens, q.device, batch)
+        _shape(idx, "idx", (batch, h_kv, budget), q.device)
+        _shape(count, "count", (batch, h_kv), q.device)
+        _need_mass(mass, "mass", batch, h_kv, block_table.shape[1] * page_size, q.device)
+        p, n, _hold = _scratch(ws, _ws_bytes(FN_DECODE_MASS, batch, h_q, h_kv, d,
+                                             block_table.shape[1], page_size, budget,
+                                             q.device.index), q.device)
+        _call_on(q.device, "jssa_decode_mass", q.data_ptr(), _ptr(k_new), _ptr(v_new),
+                 k_cache.data_ptr(), v_cache.data_ptr(), *strides, score_cache.data_ptr(),
+                 basis.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                 seq_lens.data_ptr(), batch, h_q, h_kv, d, r, num_pages, page_size, budget, scale,
+                 mass.data_ptr(), mass.shape[2], idx.data_ptr(), count.data_ptr(), out.data_ptr(),
+                 p, n)
+        return out, idx, count
     w = _ws(q.device, ws, FN_DECODE)
     p, n = w.get(workspace_size(FN_DECODE, batch, h_q, h_kv, d, block_table.shape[1], page_size,
                                 budget))
@@ -537,6 +659,151 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
          num_pages, page_size, budget, scale, idx.data_ptr(), count.data_ptr(), out.data_ptr(), p, n,
          _stream(q.device))
     return out, idx, count
+
+
+# ------------------------------------------------------------------------------------------------
+# Drafted trees and eviction
+# ------------------------------------------------------------------------------------------------
+
+TREE_MAX_NODES = 64
+
+
+def tree_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
+                k_new: Optional[torch.Tensor] = None, v_new: Optional[torch.Tensor] = None,
+                idx: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None,
+                scale: Optional[float] = None, window: int = -1,
+                out: Optional[torch.Tensor] = None,
+                ws: Optional[Workspace] = None) -> torch.Tensor:
+    """Attention of a tree of drafted tokens: query rows ``q`` bf16 ``[batch, n, h_q, d]``
+    (``n <= 64``) of nodes whose K / V rows are at cache positions ``seq_lens[b] + i`` (written
+    there by this call when ``k_new`` / ``v_new`` bf16 ``[batch, n, h_kv, d]`` are given).
+    ``parents`` int32 ``[batch, n]``: -1 follows the last committed token, ``0 <= p < i`` follows
+    node ``p``, below -1 marks an unused (padded) node, whose output is zero. A node sees itself,
+    its ancestors and the committed tokens: all of them, a sliding ``window`` ending at its own
+    logical position, or the index set ``idx`` / ``count`` of :func:`score_topk`."""
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, n, h_q, d]")
+    batch, n, h_q, d = q.shape
+    dev = q.device
+    strides, num_pages, page_size, h_kv, dc = _need_cache(k_cache, v_cache)
+    if dc != d or k_cache.device != dev:
+        raise ValueError("q and the caches must agree on the head dim and the device")
+    _need_table(block_table, seq_lens, dev, batch)
+    _need(parents, "parents", torch.int32)
+    _shape(parents, "parents", (batch, n), dev)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None:
+        _need(k_new, "k_new", torch.bfloat16)
+        _need(v_new, "v_new", torch.bfloat16)
+        _shape(k_new, "k_new", (batch, n, h_kv, d), dev)
+        _shape(v_new, "v_new", (batch, n, h_kv, d), dev)
+    if (idx is None) != (count is None):
+        raise ValueError("idx and count go together")
+    budget = 0
+    if idx is not None:
+        _need(idx, "idx", torch.int32)
+        _need(count, "count", torch.int32)
+        budget = idx.shape[-1]
+        _shape(idx, "idx", (batch, h_kv, budget), dev)
+        _shape(count, "count", (batch, h_kv), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16)
+        _shape(out, "out", (batch, n, h_q, d), dev)
+    p, nb, _hold = _scratch(ws, _ws_bytes(FN_TREE_ATTEND, batch, h_q, h_kv, d,
+                                          block_table.shape[1], page_size, n, dev.index), dev)
+    _call_on(dev, "jssa_tree_attend", q.data_ptr(), _ptr(k_new), _ptr(v_new), k_cache.data_ptr(),
+             v_cache.data_ptr(), *strides, block_table.data_ptr(), block_table.shape[1],
+             seq_lens.data_ptr(), parents.data_ptr(), _ptr(idx), _ptr(count), batch, n, h_q, h_kv,
+             d, budget, num_pages, page_size, window, scale, out.data_ptr(), p, nb)
+    return out
+
+
+def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                seq_lens: torch.Tensor, path: torch.Tensor, n_path: torch.Tensor,
+                score_cache: Optional[torch.Tensor] = None,
+                lens: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Keep the accepted nodes of a drafted tree: for ``i < n_path[b]`` the row (K, V, scoring
+    code) of position ``seq_lens[b] + path[b, i]`` moves to ``seq_lens[b] + i``. ``path`` int32
+    ``[batch, <= 64]`` (node indices), ``n_path`` int32 ``[batch]``. Returns the new lengths
+    (int32 ``[batch]``; ``seq_lens`` itself is left as it is)."""
+    strides, num_pages, page_size, h_kv, d = _need_cache(k_cache, v_cache)
+    dev = k_cache.device
+    _need_table(block_table, seq_lens, dev)
+    batch = block_table.shape[0]
+    _need(path, "path", torch.int32)
+    _need(n_path, "n_path", torch.int32)
+    _shape(path, "path", (batch, path.shape[-1]), dev)
+    _shape(n_path, "n_path", (batch,), dev)
+    code = _need_codes(score_cache, num_pages, h_kv, page_size, dev)
+    if lens is None:
+        lens = torch.empty_like(seq_lens)
+    else:
+        _need(lens, "lens", torch.int32)
+        _shape(lens, "lens", (batch,), dev)
+    _call_on(dev, "jssa_tree_commit", k_cache.data_ptr(), v_cache.data_ptr(), *strides,
+             _ptr(score_cache), code, block_table.data_ptr(), block_table.shape[1],
+             seq_lens.data_ptr(), path.data_ptr(), n_path.data_ptr(), path.shape[1], batch, h_kv, d,
+             num_pages, page_size, lens.data_ptr())
+    return lens
+
+
+def evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+          block_table: torch.Tensor, seq_lens: torch.Tensor, keep: int, recent: int = 0,
+          score_cache: Optional[torch.Tensor] = None,
+          dst_block_table: Optional[torch.Tensor] = None,
+          mass_out: Optional[torch.Tensor] = None, idx: Optional[torch.Tensor] = None,
+          count: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None):
+    """Cut every sequence to at most ``keep`` positions per KV head: the last ``recent`` ones and
+    those of the largest accumulated attention ``mass`` (float32
+    ``[batch, h_kv, >= max_pages * page_size]``; ties to the lower position). The kept rows (K, V,
+    scoring codes, mass) move, in order, to positions 0, 1, ... of ``dst_block_table`` (in place
+    when None, else pages that no sequence of this call reads) and of ``mass_out`` (``mass`` when
+    None), whose entries from there to the old length become zero. Returns
+    ``(idx, count, lens)``: the kept positions int32 ``[batch, h_kv, keep]`` (ascending, -1
+    padded), their number, and the new lengths int32 ``[batch]`` (``seq_lens`` is left as it is)."""
+    strides, num_pages, page_size, h_kv, d = _need_cache(k_cache, v_cache)
+    dev = k_cache.device
+    _need_table(block_table, seq_lens, dev)
+    batch, max_pages = block_table.shape
+    _need_mass(mass, "mass", batch, h_kv, max_pages * page_size, dev)
+    if mass_out is None:
+        mass_out = mass
+    else:
+        _need_mass(mass_out, "mass_out", batch, h_kv, max_pages * page_size, dev)
+        if mass_out.shape[2] != mass.shape[2]:
+            raise ValueError("mass and mass_out must have the same shape")
+    code = _need_codes(score_cache, num_pages, h_kv, page_size, dev)
+    if dst_block_table is None:
+        dst_block_table = block_table
+    else:
+        _need_table(dst_block_table, None, dev, batch, "dst_block_table")
+    if idx is None:
+        idx = torch.empty((batch, h_kv, keep), dtype=torch.int32, device=dev)
+    else:
+        _need(idx, "idx", torch.int32)
+        _shape(idx, "idx", (batch, h_kv, keep), dev)
+    if count is None:
+        count = torch.empty((batch, h_kv), dtype=torch.int32, device=dev)
+    else:
+        _need(count, "count", torch.int32)
+        _shape(count, "count", (batch, h_kv), dev)
+    if lens is None:
+        lens = torch.empty_like(seq_lens)
+    else:
+        _need(lens, "lens", torch.int32)
+        _shape(lens, "lens", (batch,), dev)
+    _call_on(dev, "jssa_evict", mass.data_ptr(), mass.shape[2], k_cache.data_ptr(),
+             v_cache.data_ptr(), *strides, _ptr(score_cache), code, block_table.data_ptr(),
+             max_pages, dst_block_table.data_ptr(), dst_block_table.shape[1], seq_lens.data_ptr(),
+             batch, h_kv, d, num_pages, page_size, keep, recent, idx.data_ptr(), count.data_ptr(),
+             mass_out.data_ptr(), lens.data_ptr())
+    return idx, count, lens
 
 
 def set_wait_limit(cycles: int) -> int:
@@ -555,9 +822,14 @@ def device_error(clear: bool = True, device=None) -> int:
 
 class PagedLayer:
     """One attention layer's decode state: paged bf16 K/V caches, the FP8 scoring cache, the
-    basis and the per-step buffers, with ``step`` running one JSSA decode step."""
+    basis and the per-step buffers, with ``step`` running one JSSA decode step. ``draft`` and
+    ``commit`` run a tree of drafted tokens and keep its accepted path; with ``track_mass`` every
+    ``step`` and ``dense`` adds the positions' attention weights to ``mass``, and ``evict`` cuts
+    the cache down by them. ``seq_lens`` is updated in place by ``commit`` and ``evict`` and
+    otherwise belongs to the caller."""
 
-    def __init__(self, k_cache, v_cache, block_table, seq_lens, basis, budget, scale=None):
+    def __init__(self, k_cache, v_cache, block_table, seq_lens, basis, budget, scale=None,
+                 track_mass=False):
         self.k_cache, self.v_cache = k_cache, v_cache
         self.block_table, self.seq_lens = block_table, seq_lens
         self.basis = basis
@@ -573,6 +845,11 @@ class PagedLayer:
         self.count = torch.empty((batch, h_kv), dtype=torch.int32, device=k_cache.device)
         self.ws = Workspace(k_cache.device)        # decode steps
         self.ws_dense = Workspace(k_cache.device)  # dense baseline
+        # running attention mass of every position (what `evict` goes by); None: not kept
+        self.mass = (torch.zeros((batch, h_kv, block_table.shape[1] * page_size),
+                                 dtype=torch.float32, device=k_cache.device) if track_mass else None)
+        self.ws_mass = Workspace(k_cache.device)   # steps that keep the mass
+        self.ws_tree = Workspace(k_cache.device)   # drafted trees
 
     def prefill_scores(self, chunk_pages: int = 4096) -> None:
         """Store the scoring code of every cached position (all slots of every page)."""
@@ -587,11 +864,60 @@ class PagedLayer:
     def step(self, q, k_new=None, v_new=None, out=None):
         return decode(q, k_new, v_new, self.k_cache, self.v_cache, self.score_cache, self.basis,
                       self.block_table, self.seq_lens, self.budget, self.scale, out, self.idx,
-                      self.count, self.ws)
+                      self.count, self.ws if self.mass is None else self.ws_mass, self.mass)
 
     def dense(self, q, out=None, window=-1):
         return dense_decode(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens,
-                            self.scale, window, out, self.ws_dense)
+                            self.scale, window, out,
+                            self.ws_dense if self.mass is None else self.ws_mass, self.mass)
+
+    def draft(self, q, k_new, v_new, parents, out=None, window=-1, sparse=False):
+        """Attention of a tree of drafted tokens that follow the ``seq_lens`` committed ones
+        (:func:`tree_attend`); the nodes' K, V and scoring codes are stored at positions
+        ``seq_lens[b] + i``. ``sparse``: the context is the top-B selection of the mean query of
+        the tree's used nodes, one set per KV head for the whole tree."""
+        batch, n, h_kv, d = k_new.shape
+        slots = self._node_slots(parents)
+        store(k_new.view(batch * n, h_kv, d), slots.view(-1), self.basis, self.score_cache)
+        idx = count = None
+        if sparse:
+            used = (parents >= -1).to(torch.float32)
+            mean = (torch.einsum("bnhd,bn->bhd", q.float(), used)
+                    / used.sum(1).clamp(min=1.0)[:, None, None]).to(torch.bfloat16)
+            idx, count = score_topk(mean, self.basis, self.score_cache, self.block_table,
+                                    self.seq_lens, self.budget, self.idx, self.count)
+        return tree_attend(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens, parents,
+                           k_new, v_new, idx, count, self.scale, window, out, self.ws_tree)
+
+    def _node_slots(self, parents):
+        """Flat cache slots of the tree's nodes (int64 ``[batch, n]``; -1 where a node is unused
+        or beyond the block table)."""
+        n = parents.shape[1]
+        max_pages = self.block_table.shape[1]
+        pos = self.seq_lens.long()[:, None] + torch.arange(n, device=parents.device)[None]
+        ok = (parents >= -1) & (pos < max_pages * self.page_size)
+        page = torch.gather(self.block_table, 1,
+                            (pos // self.page_size).clamp(max=max_pages - 1)).long()
+        return torch.where(ok, page * self.page_size + pos % self.page_size, -1)
+
+    def commit(self, path, n_path):
+        """Keep the accepted nodes ``path[b, :n_path[b]]`` of the last drafted tree
+        (:func:`tree_commit`): ``seq_lens`` grows by ``n_path``."""
+        lens = tree_commit(self.k_cache, self.v_cache, self.block_table, self.seq_lens, path, n_path,
+                           self.score_cache)
+        self.seq_lens.copy_(lens)
+        return self.seq_lens
+
+    def evict(self, keep, recent=0):
+        """Cut every sequence to ``keep`` positions per KV head by the accumulated mass, in place
+        (:func:`evict`); ``seq_lens`` becomes at most ``keep``. Returns the kept positions and
+        their number."""
+        if self.mass is None:
+            raise ValueError("evict needs track_mass=True")
+        idx, count, lens = evict(self.mass, self.k_cache, self.v_cache, self.block_table,
+                                 self.seq_lens, keep, recent, self.score_cache)
+        self.seq_lens.copy_(lens)
+        return idx, count
 
 
 class HostPipeline:

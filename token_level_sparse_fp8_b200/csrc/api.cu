@@ -243,6 +243,26 @@ int jssa_workspace_size(int fn, int batch, int h_q, int h_kv, int d, int max_pag
       if (fn == JSSA_FN_MLA_DECODE)
         *bytes = align256(*bytes) + score_ws_bytes(batch, 1, max_seq_len, page_size, 576);
       return JSSA_OK;
+    case JSSA_FN_DENSE_DECODE_MASS: {
+      if (!supported_d(d) || h_q / h_kv > jssa::kAttendMaxG) return JSSA_ERR_UNSUPPORTED;
+      const int span = (budget > 0 && budget < max_seq_len) ? budget : max_seq_len;
+      *bytes = jssa::plan_attend_mass(batch * h_kv, span, h_q / h_kv, d).ws_bytes;
+      return JSSA_OK;
+    }
+    case JSSA_FN_INDEXED_ATTEND_MASS:
+    case JSSA_FN_DECODE_MASS:
+      if (budget <= 0) return JSSA_ERR_SHAPE;
+      if (!supported_d(d) || h_q / h_kv > jssa::kAttendMaxG) return JSSA_ERR_UNSUPPORTED;
+      *bytes = jssa::plan_attend_mass(batch * h_kv, budget, h_q / h_kv, d).ws_bytes;
+      if (fn == JSSA_FN_DECODE_MASS)
+        *bytes = align256(*bytes) + score_ws_bytes(batch, h_kv, max_seq_len, page_size, d);
+      return JSSA_OK;
+    case JSSA_FN_TREE_ATTEND:  // budget carries the nodes per sequence
+      if (budget < 0) return JSSA_ERR_SHAPE;
+      if (!supported_d(d) || h_q / h_kv > jssa::kAttendMaxG || budget > jssa::kTreeMaxNodes)
+        return JSSA_ERR_UNSUPPORTED;
+      *bytes = jssa::tree_ws_bytes(batch, budget, h_q, h_kv, d);
+      return JSSA_OK;
     case JSSA_FN_DENSE_DECODE: {
       const int span = (budget > 0 && budget < max_seq_len) ? budget : max_seq_len;
       *bytes = attend_plan_dense(batch, h_q, h_kv, d, span).ws_bytes;
@@ -462,6 +482,163 @@ int jssa_dense_decode(const jssa_bf16* q, const jssa_bf16* k_cache, const jssa_b
   return cuda_status(jssa::launch_attend(a, false, plan, true, as_stream(stream)));
 }
 
+static int check_mass(const float* mass, int64_t mass_stride, int max_pages, int page_size) {
+  if (!mass) return JSSA_ERR_NULL;
+  if ((uintptr_t)mass & 3u) return JSSA_ERR_ALIGN;
+  if (mass_stride < (int64_t)max_pages * page_size) return JSSA_ERR_SHAPE;
+  return JSSA_OK;
+}
+
+int jssa_indexed_attend_mass(const jssa_bf16* q, const jssa_bf16* k_cache, const jssa_bf16* v_cache,
+                             int64_t kv_page_stride, int64_t kv_slot_stride,
+                             int64_t kv_head_stride, const int32_t* block_table, int max_pages,
+                             const int32_t* idx, const int32_t* count, int batch, int h_q, int h_kv,
+                             int d, int budget, int64_t num_pages, int page_size,
+                             float softmax_scale, float* mass, int64_t mass_stride, jssa_bf16* out,
+                             void* ws, size_t ws_bytes, jssa_stream_t stream) {
+  if (budget <= 0) return JSSA_ERR_SHAPE;
+  int st = check_attend_common(q, k_cache, v_cache, kv_page_stride, kv_slot_stride,
+                               kv_head_stride, block_table, max_pages, batch, h_q, h_kv, d,
+                               num_pages, page_size, out);
+  if (!st && (int64_t)batch * h_kv > 65535) return JSSA_ERR_UNSUPPORTED;  // one grid row per pair
+  if (st || batch == 0) return st;
+  if (!idx || !count) return JSSA_ERR_NULL;
+  if ((st = check_mass(mass, mass_stride, max_pages, page_size))) return st;
+  const jssa::MassPlan plan = jssa::plan_attend_mass(batch * h_kv, budget, h_q / h_kv, d);
+  if (!ws || ws_bytes < plan.ws_bytes) return JSSA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return JSSA_ERR_ALIGN;
+  AttendArgs a = {};
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.page_stride = kv_page_stride; a.slot_stride = kv_slot_stride; a.head_stride = kv_head_stride;
+  a.block_table = block_table; a.max_pages = max_pages; a.idx = idx; a.count = count;
+  a.batch = batch; a.h_q = h_q; a.h_kv = h_kv; a.d = d; a.budget = budget;
+  a.num_pages = num_pages; a.page_size = page_size; a.scale = softmax_scale; a.out = out;
+  a.ws = ws; a.mass = mass; a.mass_stride = mass_stride;
+  return cuda_status(jssa::launch_attend_mass(a, true, plan, false, as_stream(stream)));
+}
+
+int jssa_dense_decode_mass(const jssa_bf16* q, const jssa_bf16* k_cache, const jssa_bf16* v_cache,
+                           int64_t kv_page_stride, int64_t kv_slot_stride, int64_t kv_head_stride,
+                           const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                           int batch, int h_q, int h_kv, int d, int64_t num_pages, int page_size,
+                           int window, float softmax_scale, float* mass, int64_t mass_stride,
+                           jssa_bf16* out, void* ws, size_t ws_bytes, jssa_stream_t stream) {
+  int st = check_attend_common(q, k_cache, v_cache, kv_page_stride, kv_slot_stride,
+                               kv_head_stride, block_table, max_pages, batch, h_q, h_kv, d,
+                               num_pages, page_size, out);
+  if (!st && (int64_t)batch * h_kv > 65535) return JSSA_ERR_UNSUPPORTED;
+  if (st || batch == 0) return st;
+  if (!seq_lens) return JSSA_ERR_NULL;
+  if ((st = check_mass(mass, mass_stride, max_pages, page_size))) return st;
+  int span = max_pages * page_size;
+  if (window > 0 && window < span) span = window;
+  const jssa::MassPlan plan = jssa::plan_attend_mass(batch * h_kv, span, h_q / h_kv, d);
+  if (!ws || ws_bytes < plan.ws_bytes) return JSSA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return JSSA_ERR_ALIGN;
+  AttendArgs a = {};
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.page_stride = kv_page_stride; a.slot_stride = kv_slot_stride; a.head_stride = kv_head_stride;
+  a.block_table = block_table; a.max_pages = max_pages; a.seq_lens = seq_lens;
+  a.window = window; a.batch = batch; a.h_q = h_q; a.h_kv = h_kv; a.d = d; a.budget = 0;
+  a.num_pages = num_pages; a.page_size = page_size; a.scale = softmax_scale; a.out = out;
+  a.ws = ws; a.mass = mass; a.mass_stride = mass_stride;
+  return cuda_status(jssa::launch_attend_mass(a, false, plan, true, as_stream(stream)));
+}
+
+static int check_move(const jssa_bf16* k_cache, const jssa_bf16* v_cache, int64_t ps, int64_t ss,
+                      int64_t hs, const uint8_t* score_cache, int score_bytes,
+                      const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
+                      int h_kv, int d, int64_t num_pages, int page_size, const int32_t* lens_out) {
+  if (batch < 0 || h_kv <= 0) return JSSA_ERR_SHAPE;
+  if (!supported_d(d)) return JSSA_ERR_UNSUPPORTED;
+  if ((int64_t)batch * h_kv > INT32_MAX) return JSSA_ERR_SHAPE;
+  int st = check_paging(max_pages, num_pages, page_size);
+  if (st) return st;
+  if (score_cache && score_bytes != 16 && score_bytes != 32 && score_bytes != 64)
+    return JSSA_ERR_UNSUPPORTED;
+  if (batch == 0) return JSSA_OK;
+  if (!block_table || !seq_lens || !lens_out) return JSSA_ERR_NULL;
+  if ((st = check_kv(k_cache, v_cache, ps, ss, hs, h_kv, d, page_size))) return st;
+  if (score_cache && !aligned16(score_cache)) return JSSA_ERR_ALIGN;
+  if (lens_out == seq_lens) return JSSA_ERR_SHAPE;
+  return JSSA_OK;
+}
+
+int jssa_evict(const float* mass, int64_t mass_stride, jssa_bf16* k_cache, jssa_bf16* v_cache,
+               int64_t kv_page_stride, int64_t kv_slot_stride, int64_t kv_head_stride,
+               uint8_t* score_cache, int score_bytes, const int32_t* block_table, int max_pages,
+               const int32_t* dst_block_table, int dst_max_pages, const int32_t* seq_lens, int batch,
+               int h_kv, int d, int64_t num_pages, int page_size, int keep, int recent, int32_t* idx,
+               int32_t* count, float* mass_out, int32_t* lens_out, jssa_stream_t stream) {
+  if (keep <= 0 || recent < 0 || recent > keep) return JSSA_ERR_SHAPE;
+  int st = check_move(k_cache, v_cache, kv_page_stride, kv_slot_stride, kv_head_stride, score_cache,
+                      score_bytes, block_table, max_pages, seq_lens, batch, h_kv, d, num_pages,
+                      page_size, lens_out);
+  if (st) return st;
+  if ((st = check_paging(dst_max_pages, num_pages, page_size)) || batch == 0) return st;
+  if (!dst_block_table || !idx || !count) return JSSA_ERR_NULL;
+  if ((st = check_mass(mass, mass_stride, max_pages, page_size))) return st;
+  if ((st = check_mass(mass_out, mass_stride, max_pages, page_size))) return st;
+  // the same table under another width would be read with the wrong row stride
+  if (dst_block_table == block_table && dst_max_pages != max_pages) return JSSA_ERR_SHAPE;
+  const jssa::RowMove m = {k_cache, v_cache, kv_page_stride, kv_slot_stride, kv_head_stride,
+                           score_cache, score_cache ? score_bytes : 0, block_table, max_pages,
+                           seq_lens, batch, h_kv, d, num_pages, page_size, lens_out};
+  const jssa::EvictArgs e = {mass, mass_out, mass_stride, keep, recent, dst_block_table,
+                             dst_max_pages, idx, count};
+  return cuda_status(jssa::launch_evict(m, e, as_stream(stream)));
+}
+
+int jssa_tree_commit(jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                     int64_t kv_slot_stride, int64_t kv_head_stride, uint8_t* score_cache,
+                     int score_bytes, const int32_t* block_table, int max_pages,
+                     const int32_t* seq_lens, const int32_t* path, const int32_t* n_path,
+                     int max_path, int batch, int h_kv, int d, int64_t num_pages, int page_size,
+                     int32_t* lens_out, jssa_stream_t stream) {
+  if (max_path < 0) return JSSA_ERR_SHAPE;
+  if (max_path > jssa::kTreeMaxNodes) return JSSA_ERR_UNSUPPORTED;
+  int st = check_move(k_cache, v_cache, kv_page_stride, kv_slot_stride, kv_head_stride, score_cache,
+                      score_bytes, block_table, max_pages, seq_lens, batch, h_kv, d, num_pages,
+                      page_size, lens_out);
+  if (st || batch == 0) return st;
+  if ((max_path > 0 && !path) || !n_path) return JSSA_ERR_NULL;
+  const jssa::RowMove m = {k_cache, v_cache, kv_page_stride, kv_slot_stride, kv_head_stride,
+                           score_cache, score_cache ? score_bytes : 0, block_table, max_pages,
+                           seq_lens, batch, h_kv, d, num_pages, page_size, lens_out};
+  return cuda_status(jssa::launch_commit(m, path, n_path, max_path, as_stream(stream)));
+}
+
+int jssa_tree_attend(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_new,
+                     jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                     int64_t kv_slot_stride, int64_t kv_head_stride, const int32_t* block_table,
+                     int max_pages, const int32_t* seq_lens, const int32_t* parents,
+                     const int32_t* idx, const int32_t* count, int batch, int n_nodes, int h_q,
+                     int h_kv, int d, int budget, int64_t num_pages, int page_size, int window,
+                     float softmax_scale, jssa_bf16* out, void* ws, size_t ws_bytes,
+                     jssa_stream_t stream) {
+  if (n_nodes < 0) return JSSA_ERR_SHAPE;
+  if (n_nodes > jssa::kTreeMaxNodes) return JSSA_ERR_UNSUPPORTED;
+  if (idx && (budget <= 0 || window > 0)) return JSSA_ERR_SHAPE;
+  // an empty tree is a no-op
+  int st = check_attend_common(q, k_cache, v_cache, kv_page_stride, kv_slot_stride,
+                               kv_head_stride, block_table, max_pages, n_nodes ? batch : batch < 0 ? -1 : 0,
+                               h_q, h_kv, d, num_pages, page_size, out);
+  if (!st && (int64_t)batch * h_kv > 65535) return JSSA_ERR_UNSUPPORTED;
+  if (st || batch == 0 || n_nodes == 0) return st;
+  if (!seq_lens || !parents || (idx && !count) || (k_new == nullptr) != (v_new == nullptr))
+    return JSSA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out) || (k_new && (!aligned16(k_new) || !aligned16(v_new))))
+    return JSSA_ERR_ALIGN;
+  const size_t need = jssa::tree_ws_bytes(batch, n_nodes, h_q, h_kv, d);
+  if (need && (!ws || ws_bytes < need)) return JSSA_ERR_WORKSPACE;
+  if (need && !aligned16(ws)) return JSSA_ERR_ALIGN;
+  const jssa::TreeArgs a = {q, k_new, v_new, k_cache, v_cache, kv_page_stride, kv_slot_stride,
+                            kv_head_stride, block_table, max_pages, seq_lens, parents, idx, count,
+                            batch, n_nodes, h_q, h_kv, d, idx ? budget : 0, num_pages, page_size,
+                            window, softmax_scale, out, ws};
+  return cuda_status(jssa::launch_tree(a, as_stream(stream)));
+}
+
 static int check_mla_kv(const jssa_bf16* q, const void* kv_cache, int64_t kv_page_stride,
                         int64_t kv_slot_stride, const jssa_bf16* out) {
   if (!q || !kv_cache || !out) return JSSA_ERR_NULL;
@@ -560,14 +737,16 @@ int jssa_gather_kv(const jssa_bf16* k_cache, const jssa_bf16* v_cache, int64_t k
                                          lens_out, as_stream(stream)));
 }
 
-int jssa_decode(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_new,
-                jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
-                int64_t kv_slot_stride, int64_t kv_head_stride, uint8_t* score_cache,
-                const float* basis, const int32_t* block_table, int max_pages,
-                const int32_t* seq_lens, int batch, int h_q, int h_kv, int d, int r,
-                int64_t num_pages, int page_size, int budget, float softmax_scale,
-                int32_t* idx, int32_t* count, jssa_bf16* out, void* ws, size_t ws_bytes,
-                jssa_stream_t stream) {
+// The whole step; mass null: without the running sums.
+static int decode_step(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_new,
+                       jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                       int64_t kv_slot_stride, int64_t kv_head_stride, uint8_t* score_cache,
+                       const float* basis, const int32_t* block_table, int max_pages,
+                       const int32_t* seq_lens, int batch, int h_q, int h_kv, int d, int r,
+                       int64_t num_pages, int page_size, int budget, float softmax_scale,
+                       bool with_mass, float* mass, int64_t mass_stride, int32_t* idx,
+                       int32_t* count, jssa_bf16* out, void* ws, size_t ws_bytes,
+                       jssa_stream_t stream) {
   int st = check_score_args(q, basis, score_cache, block_table, max_pages, seq_lens, batch, h_q,
                             h_kv, d, r, num_pages, page_size, budget, idx, count);
   if (st) return st;
@@ -576,11 +755,15 @@ int jssa_decode(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_n
   if (st || batch == 0) return st;
   if ((k_new == nullptr) != (v_new == nullptr)) return JSSA_ERR_NULL;
   if (k_new && (!aligned16(k_new) || !aligned16(v_new))) return JSSA_ERR_ALIGN;
+  if (with_mass && (st = check_mass(mass, mass_stride, max_pages, page_size))) return st;
   const jssa::AttendPlan plan = attend_plan_indexed(batch, h_q, h_kv, d, budget);
+  jssa::MassPlan mplan = {};
+  if (with_mass) mplan = jssa::plan_attend_mass(batch * h_kv, budget, h_q / h_kv, d);
   // workspace: [attention tickets + partials | score candidates]; the score kernel clears the
   // tickets of every (sequence, KV head) before the attention runs, so no prior clearing is needed
+  // (the mass form keeps partials and scores there, and no tickets)
   const size_t score_ws = score_ws_bytes(batch, h_kv, max_pages * page_size, page_size, d);
-  const size_t attend_bytes = align256(plan.ws_bytes);
+  const size_t attend_bytes = align256(with_mass ? mplan.ws_bytes : plan.ws_bytes);
   if (!ws || ws_bytes < attend_bytes + score_ws) return JSSA_ERR_WORKSPACE;
   if (!aligned16(ws)) return JSSA_ERR_ALIGN;
   void* attend_ws = ws;
@@ -595,7 +778,7 @@ int jssa_decode(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_n
   cudaError_t e = jssa::launch_score_topk(q, basis, score_cache, block_table, max_pages, seq_lens,
                                           batch, h_q, h_kv, d, r, num_pages, page_size, budget,
                                           idx, count, cand_ws,
-                                          plan.ws_bytes ? static_cast<int*>(attend_ws) : nullptr,
+                                          plan.ws_bytes && !with_mass ? static_cast<int*>(attend_ws) : nullptr,
                                           k_new ? &sn : nullptr, true, s);
   if (e != cudaSuccess) return (int)e;
   AttendArgs a = {};
@@ -604,8 +787,40 @@ int jssa_decode(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_n
   a.block_table = block_table; a.max_pages = max_pages; a.idx = idx; a.count = count;
   a.batch = batch; a.h_q = h_q; a.h_kv = h_kv; a.d = d; a.budget = budget;
   a.num_pages = num_pages; a.page_size = page_size; a.scale = softmax_scale; a.out = out;
+  if (with_mass) {
+    a.ws = attend_ws; a.mass = mass; a.mass_stride = mass_stride;
+    return cuda_status(jssa::launch_attend_mass(a, true, mplan, true, s));
+  }
   a.ws = plan.ws_bytes ? attend_ws : nullptr;
   return cuda_status(jssa::launch_attend(a, true, plan, true, s));
+}
+
+int jssa_decode(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_new,
+                jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                int64_t kv_slot_stride, int64_t kv_head_stride, uint8_t* score_cache,
+                const float* basis, const int32_t* block_table, int max_pages,
+                const int32_t* seq_lens, int batch, int h_q, int h_kv, int d, int r,
+                int64_t num_pages, int page_size, int budget, float softmax_scale,
+                int32_t* idx, int32_t* count, jssa_bf16* out, void* ws, size_t ws_bytes,
+                jssa_stream_t stream) {
+  return decode_step(q, k_new, v_new, k_cache, v_cache, kv_page_stride, kv_slot_stride,
+                     kv_head_stride, score_cache, basis, block_table, max_pages, seq_lens, batch,
+                     h_q, h_kv, d, r, num_pages, page_size, budget, softmax_scale, false, nullptr, 0,
+                     idx, count, out, ws, ws_bytes, stream);
+}
+
+int jssa_decode_mass(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16* v_new,
+                     jssa_bf16* k_cache, jssa_bf16* v_cache, int64_t kv_page_stride,
+                     int64_t kv_slot_stride, int64_t kv_head_stride, uint8_t* score_cache,
+                     const float* basis, const int32_t* block_table, int max_pages,
+                     const int32_t* seq_lens, int batch, int h_q, int h_kv, int d, int r,
+                     int64_t num_pages, int page_size, int budget, float softmax_scale, float* mass,
+                     int64_t mass_stride, int32_t* idx, int32_t* count, jssa_bf16* out, void* ws,
+                     size_t ws_bytes, jssa_stream_t stream) {
+  return decode_step(q, k_new, v_new, k_cache, v_cache, kv_page_stride, kv_slot_stride,
+                     kv_head_stride, score_cache, basis, block_table, max_pages, seq_lens, batch,
+                     h_q, h_kv, d, r, num_pages, page_size, budget, softmax_scale, true, mass,
+                     mass_stride, idx, count, out, ws, ws_bytes, stream);
 }
 
 int jssa_decode_host(const jssa_bf16* q_host, const jssa_bf16* k_new_host,

@@ -19,6 +19,9 @@
 //   * Online softmax in the log2 domain; warps merge in shared memory; CTAs of one (b, h) merge
 //     through fp32 partials (m, l, o) in the workspace, the last CTA to take the ticket combines
 //     them, writes the bf16 output and resets the ticket.
+//   * Attention mass (MASS instances): the same body also writes every score (log2 units, fp32) of
+//     its positions to the workspace, always leaves (m, l, o) partials, and a second kernel merges
+//     them and adds sum_g softmax_g(t) to the running sums (see mass_kernel below).
 #include <float.h>
 
 #include "common.cuh"
@@ -50,7 +53,10 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   return r;
 }
 
-template <int D, bool INDEXED>
+// Floats of one partial row: m, l, o[d].
+__host__ __device__ constexpr int part_row(int d) { return d + 2; }
+
+template <int D, bool INDEXED, bool MASS>
 __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
     attend_kernel(AttendArgs a, int chunk, int splits) {
   static_assert(D == 128 || D == 256, "head dim");
@@ -201,6 +207,18 @@ __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
     x[1] = ok0 ? s[1] * scale_log2 : -INFINITY;
     x[2] = ok1 ? s[2] * scale_log2 : -INFINITY;
     x[3] = ok1 ? s[3] * scale_log2 : -INFINITY;
+    if (MASS) {  // scores [pair][position of the walk][G]
+      float* sc = a.scores + ((int64_t)pair * a.score_span + j_begin + j0) * G;
+      const int h0 = 2 * t, h1 = 2 * t + 1;
+      if (j0 + g < n_mine) {
+        if (h0 < G) sc[g * G + h0] = x[0];
+        if (h1 < G) sc[g * G + h1] = x[1];
+      }
+      if (j0 + g + 8 < n_mine) {
+        if (h0 < G) sc[(g + 8) * G + h0] = x[2];
+        if (h1 < G) sc[(g + 8) * G + h1] = x[3];
+      }
+    }
     float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) {
@@ -271,7 +289,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
   const int64_t out_base = ((int64_t)b * a.h_q + (int64_t)h * G) * D;
   float* part = nullptr;
   int* tickets = nullptr;
-  if (splits > 1) {
+  if (MASS) {
+    part = reinterpret_cast<float*>(a.ws);
+  } else if (splits > 1) {
     tickets = reinterpret_cast<int*>(a.ws);
     const int64_t n_pairs = (int64_t)gridDim.y;
     part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws) + ((n_pairs * 4 + 255) / 256) * 256);
@@ -290,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
         l += f * s_l[w][row];
       }
     }
-    if (splits == 1) {
+    if (!MASS && splits == 1) {
       a.out[out_base + (int64_t)row * D + dim] = f_to_bf16(l > 0.f ? acc / l : 0.f);
     } else {
       float* pp = part + (((int64_t)pair * splits + split) * G + row) * (D + 2);
@@ -301,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
       }
     }
   }
-  if (splits == 1) return;
+  if (MASS || splits == 1) return;
 
   // ---- last CTA of this (b, h) combines the partials -----------------------------------------
   __threadfence();
@@ -364,9 +384,102 @@ __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
   if (tid == 0) tickets[pair] = 0;
 }
 
-template <int D, bool INDEXED>
+// Second kernel of the mass form: merges the splits' partials into the output and adds each
+// attended position's weight to its running sum,
+//   mass[pair][t] += sum_g 2^(x_g(t) - M_g) / l_g,
+// with M_g, l_g the merged maximum and sum of query head g. Grid (position blocks, pairs); every
+// block re-reads the pair's few (m, l). All sums in fp32.
+constexpr int kMassThreads = 256;
+constexpr int kMassSpan = 1024;  // positions per block
+
+template <int GV, bool INDEXED>
+__global__ void __launch_bounds__(kMassThreads) mass_kernel(AttendArgs a, int splits) {
+  __shared__ float s_m[kAttendMaxG], s_inv[kAttendMaxG];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pair = blockIdx.y, b = pair / a.h_kv;
+  const int G = GV > 0 ? GV : a.h_q / a.h_kv;
+  const int row_f = part_row(a.d);
+  pdl_wait();
+  const float* part = reinterpret_cast<const float*>(a.ws) + (int64_t)pair * splits * G * row_f;
+  if (warp < G) {
+    float m = -INFINITY;
+    for (int sp = lane; sp < splits; sp += 32) m = fmaxf(m, part[((int64_t)sp * G + warp) * row_f]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    if (m != -INFINITY)
+      for (int sp = lane; sp < splits; sp += 32) {
+        const float* p = part + ((int64_t)sp * G + warp) * row_f;
+        l += fast_exp2(p[0] - m) * p[1];
+      }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_inv[warp] = l > 0.f ? 1.f / l : 0.f;
+    }
+  }
+  __syncthreads();
+  // this block's share of the output elements
+  for (int e = blockIdx.x * kMassThreads + tid; e < G * a.d; e += gridDim.x * kMassThreads) {
+    const int g = e / a.d, dim = e % a.d;
+    float acc = 0.f;
+    if (s_m[g] != -INFINITY)
+      for (int sp = 0; sp < splits; ++sp) {
+        const float* p = part + ((int64_t)sp * G + g) * row_f;
+        acc += fast_exp2(p[0] - s_m[g]) * p[2 + dim];
+      }
+    a.out[(int64_t)pair * G * a.d + e] = f_to_bf16(acc * s_inv[g]);
+  }
+  int n, lo = 0;
+  if (INDEXED) {
+    n = a.count[pair];
+    n = n < 0 ? 0 : (n > a.budget ? a.budget : n);
+  } else {
+    const int max_len = a.max_pages * a.page_size;
+    int L = a.seq_lens[b];
+    L = L < 0 ? 0 : (L > max_len ? max_len : L);
+    lo = a.window > 0 ? max(0, L - a.window) : 0;
+    n = L - lo;
+  }
+  for (int j = blockIdx.x * kMassSpan + tid; j < n; j += kMassThreads) {
+    if (j >= (blockIdx.x + 1) * kMassSpan) break;
+    const float* x = a.scores + ((int64_t)pair * a.score_span + j) * G;
+    float w = 0.f;
+    bool any = false;
+    for (int g = 0; g < G; ++g) {
+      const float xg = x[g];
+      if (xg != -INFINITY) {
+        w += fast_exp2(xg - s_m[g]) * s_inv[g];
+        any = true;
+      }
+    }
+    if (!any) continue;  // an unusable page or position (flagged by the first kernel)
+    const int pos = INDEXED ? a.idx[(int64_t)pair * a.budget + j] : lo + j;
+    a.mass[(int64_t)pair * a.mass_stride + pos] += w;
+  }
+}
+
+template <bool INDEXED>
+cudaError_t launch_mass(const AttendArgs& a, const AttendPlan& plan, int span, cudaStream_t s) {
+  const int G = a.h_q / a.h_kv;
+  auto kern = G == 4 ? mass_kernel<4, INDEXED> : G == 8 ? mass_kernel<8, INDEXED>
+            : G == 2 ? mass_kernel<2, INDEXED> : mass_kernel<0, INDEXED>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((span + kMassSpan - 1) / kMassSpan, a.batch * a.h_kv, 1);
+  cfg.blockDim = dim3(kMassThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, plan.splits);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <int D, bool INDEXED, bool MASS>
 cudaError_t launch_t(const AttendArgs& a, const AttendPlan& plan, bool pdl, cudaStream_t s) {
-  auto kern = attend_kernel<D, INDEXED>;
+  auto kern = attend_kernel<D, INDEXED, MASS>;
   constexpr int kRingBytes = Ring<D>::kBytes;
   static_assert(kRingBytes >= kWarps * kAttendMaxG * D * (int)sizeof(float), "merge buffer");
   cudaError_t ce = configure_kernel((const void*)kern, kRingBytes, false);
@@ -416,12 +529,40 @@ cudaError_t launch_attend(const AttendArgs& a, bool indexed, const AttendPlan& p
                           cudaStream_t s) {
   if (a.batch * a.h_kv == 0) return cudaSuccess;
   if (a.d == 128)
-    return indexed ? attend_detail::launch_t<128, true>(a, plan, pdl, s)
-                   : attend_detail::launch_t<128, false>(a, plan, pdl, s);
+    return indexed ? attend_detail::launch_t<128, true, false>(a, plan, pdl, s)
+                   : attend_detail::launch_t<128, false, false>(a, plan, pdl, s);
   if (a.d == 256)
-    return indexed ? attend_detail::launch_t<256, true>(a, plan, pdl, s)
-                   : attend_detail::launch_t<256, false>(a, plan, pdl, s);
+    return indexed ? attend_detail::launch_t<256, true, false>(a, plan, pdl, s)
+                   : attend_detail::launch_t<256, false, false>(a, plan, pdl, s);
   return cudaErrorInvalidValue;
+}
+
+MassPlan plan_attend_mass(int pairs, int positions, int group, int d) {
+  MassPlan p;
+  p.attend = plan_attend(pairs, positions, group, d);
+  p.span = positions < 1 ? 1 : positions;
+  const size_t part = (size_t)pairs * p.attend.splits * group * attend_detail::part_row(d) * sizeof(float);
+  p.scores_offset = (part + 255) / 256 * 256;
+  p.ws_bytes = p.scores_offset + (size_t)pairs * p.span * group * sizeof(float);
+  return p;
+}
+
+cudaError_t launch_attend_mass(AttendArgs a, bool indexed, const MassPlan& plan, bool pdl,
+                               cudaStream_t s) {
+  using namespace attend_detail;
+  if (a.batch * a.h_kv == 0) return cudaSuccess;
+  a.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + plan.scores_offset);
+  a.score_span = plan.span;
+  cudaError_t e = cudaErrorInvalidValue;
+  if (a.d == 128)
+    e = indexed ? launch_t<128, true, true>(a, plan.attend, pdl, s)
+                : launch_t<128, false, true>(a, plan.attend, pdl, s);
+  else if (a.d == 256)
+    e = indexed ? launch_t<256, true, true>(a, plan.attend, pdl, s)
+                : launch_t<256, false, true>(a, plan.attend, pdl, s);
+  if (e != cudaSuccess) return e;
+  return indexed ? launch_mass<true>(a, plan.attend, plan.span, s)
+                 : launch_mass<false>(a, plan.attend, plan.span, s);
 }
 
 }  // namespace jssa

@@ -81,7 +81,80 @@ struct AttendArgs {
   float scale;
   uint16_t* out;
   void* ws;
+  // mass form: scores [pair][score_span][G] in the workspace, running sums [pair][mass_stride]
+  float* scores;
+  int64_t score_span;
+  float* mass;
+  int64_t mass_stride;
 };
+
+// Attention that also adds the positions' weights to running sums: the attention's split plan,
+// the positions per pair the scores are kept for, and the workspace [partials | scores]. No
+// counters: the workspace needs no clearing.
+struct MassPlan {
+  AttendPlan attend;
+  int span;
+  size_t scores_offset, ws_bytes;
+};
+MassPlan plan_attend_mass(int pairs, int positions, int group, int d);
+cudaError_t launch_attend_mass(AttendArgs a, bool indexed, const MassPlan& plan, bool pdl,
+                               cudaStream_t s);
+
+// Attention of a tree of drafted tokens (nodes at positions seq_len + i) over the paged cache.
+constexpr int kTreeMaxNodes = 64;
+struct TreeArgs {
+  const uint16_t* q;      // [batch, n, h_q, d]
+  const uint16_t* k_new;  // [batch, n, h_kv, d], or null: the nodes' rows are in the cache
+  const uint16_t* v_new;
+  uint16_t* k_cache;
+  uint16_t* v_cache;
+  int64_t page_stride, slot_stride, head_stride;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  const int32_t* parents;  // [batch, n]
+  const int32_t* idx;      // [batch, h_kv, budget], or null: the whole context
+  const int32_t* count;
+  int batch, n, h_q, h_kv, d, budget;
+  int64_t num_pages;
+  int page_size;
+  int window;
+  float scale;
+  uint16_t* out;  // [batch, n, h_q, d]
+  void* ws;
+};
+size_t tree_ws_bytes(int batch, int n, int h_q, int h_kv, int d);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
+
+// Moves of cached rows (K, V, scoring codes, mass): the accepted nodes of a tree to consecutive
+// positions, and the kept positions of an eviction to the front of a page table.
+struct RowMove {
+  uint16_t* k_cache;
+  uint16_t* v_cache;
+  int64_t page_stride, slot_stride, head_stride;
+  uint8_t* score_cache;  // or null
+  int code_bytes;        // bytes of a scoring row (16, 32 or 64), 0 without a scoring cache
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int batch, h_kv, d;
+  int64_t num_pages;
+  int page_size;
+  int32_t* lens_out;
+};
+cudaError_t launch_commit(const RowMove& m, const int32_t* path, const int32_t* n_path, int max_path,
+                          cudaStream_t s);
+struct EvictArgs {
+  const float* mass;  // [batch, h_kv] rows of mass_stride
+  float* mass_out;
+  int64_t mass_stride;
+  int keep, recent;
+  const int32_t* dst_table;
+  int dst_max_pages;
+  int32_t* idx;
+  int32_t* count;
+};
+cudaError_t launch_evict(const RowMove& m, const EvictArgs& e, cudaStream_t s);
 
 cudaError_t launch_attend(const AttendArgs& a, bool indexed, const AttendPlan& plan, bool pdl,
                           cudaStream_t s);

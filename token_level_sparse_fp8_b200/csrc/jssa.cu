@@ -4,6 +4,8 @@
 #include "store.cu"
 #include "score_topk.cu"
 #include "attend.cu"
+#include "tree.cu"
+#include "evict.cu"
 #include "gather.cu"
 #include "mla.cu"
 #include "calib.cu"
