@@ -782,3 +782,24 @@ def test_draft_commit_step_evict(sparse):
         assert layer.seq_lens.tolist() == [min(64, x) for x in now]
         assert torch.count_nonzero(layer.mass[:, :, 64:]).item() == 0
     assert J.device_error() & ~16 == 0
+
+
+@pytest.mark.parametrize("d,n,g", [(128, 12, 4), (128, 64, 4), (256, 12, 4)])
+def test_tree_wait_timeout_then_recovery(d, n, g):
+    # a wait limit of one clock cycle: waits of a correct launch run out, the flag is raised, the
+    # call drains and returns; with the default limit the next call is correct and clean
+    J = jssa()
+    c = Paged([1500, 70], n, 2, d, seed=21)
+    parents = [random_tree(c.rng, n) for _ in range(2)]
+    q, kn, vn = c.normal(2, n, 2 * g, d).cuda(), c.normal(2, n, 2, d).cuda(), c.normal(2, n, 2, d).cuda()
+    want = J.tree_attend(q, c.k, c.v, c.bt, c.seq_lens, cuda(parents), kn, vn)
+    assert J.device_error(clear=True) == 0
+    J.set_wait_limit(1)
+    try:
+        J.tree_attend(q, c.k, c.v, c.bt, c.seq_lens, cuda(parents), kn, vn)
+        torch.cuda.synchronize()
+    finally:
+        J.set_wait_limit(0)
+    assert J.device_error(clear=True) & 32
+    out = J.tree_attend(q, c.k, c.v, c.bt, c.seq_lens, cuda(parents), kn, vn)
+    assert torch.equal(out, want) and J.device_error(clear=True) == 0

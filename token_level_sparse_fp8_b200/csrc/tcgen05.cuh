@@ -64,6 +64,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// One arrival of this thread (release: its earlier writes are visible to who waits for the phase).
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Named barriers among `n` threads of the CTA (n a multiple of 32); bar_or also returns whether
+// any of them passed true.
+__device__ __forceinline__ void bar_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool bar_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
 // Make this thread's generic-proxy writes to shared memory (st.shared, cp.async) visible to the
 // async proxy that the tensor cores read through.
 __device__ __forceinline__ void fence_proxy_async_smem() {
