@@ -14,16 +14,17 @@
 //     CTA per SM (ragged lengths balance by themselves; a CTA has at most two partial pairs). With
 //     more than 256 rows (128 at d = 256) the CTAs form row groups that walk the line side by side
 //     and share the rows through L2.
-//   * 4 producer warps copy K / V rows straight from their pages (16-byte cp.async) into a ring of
+//   * 4 copy warps bring K / V rows straight from their pages (16-byte cp.async) into a ring of
 //     stages, as 64-dimension column blocks with the 128-byte swizzle: the K-major operand of
 //     S = Q K^T and the MN-major operand of O += P V. They run ahead over pair boundaries. The
-//     nodes' rows come from k_new when given, and are written to the cache on the way.
-//   * Groups of 4 warps, one thread per query row (tensor-memory lane): S from tensor memory,
-//     online softmax in registers (fp32, lazy rescale of O), P as bf16 back over S. Q and P are the
-//     A operands from tensor memory. At d = 128 two groups: both halves of 256 rows, or, with at
-//     most 128 rows, the even and the odd tiles of the same rows, whose O are merged at the end
-//     through tensor memory (the two groups' warps share lanes). At d = 256 O takes 256 columns
-//     and one group remains.
+//     nodes' rows come from k_new when given; another warp writes them to the cache.
+//   * One warp issues the MMAs. Groups of 4 warps, one thread per query row (tensor-memory lane):
+//     S from tensor memory, online softmax in registers (fp32, lazy rescale of O), P as bf16 back
+//     to tensor memory as the A operand of P V. S of the next tile is computed while the softmax of
+//     this one runs. At d = 128 two groups: both halves of 256 rows (Q of the second one in shared
+//     memory: tensor memory is full), or, with at most 128 rows, the even and the odd tiles of the
+//     same rows, whose O are merged at the end through tensor memory (the two groups' warps share
+//     lanes). At d = 256 O takes 256 columns and one group remains.
 //   * P is rounded to bf16 (half a step, 2^-9 of a weight): the tensor cores take bf16 beside the
 //     bf16 V; the sum l is kept from the fp32 weights.
 //   * Pairs cut between CTAs leave fp32 (m, l, O) partials; a second kernel merges them.
@@ -32,6 +33,8 @@
 // the rows that see them by hand and cleared in shared memory before the MMA.
 // Every wait is bounded: after a timeout a thread goes on without waiting (all barriers still
 // match), the flag is raised, and what was issued is drained before the tensor memory is freed.
+#include <limits.h>
+
 #include "common.cuh"
 #include "tcgen05.cuh"
 
@@ -42,24 +45,35 @@ namespace tree_detail {
 constexpr int kM = 128;   // rows of an MMA = threads of a group
 constexpr int kTT = 64;   // tokens per tile (a tree of at most 64 nodes spans at most two)
 constexpr uint32_t kCols = 512;
-constexpr int kProducers = 128;
+constexpr int kCopiers = 128;  // threads that copy rows: 16 of a tile per warp
+// Row offsets are looked up for kBatch tiles of a pair at once, two batches ahead of the copies: the
+// dependent loads (index set, page table) take microseconds under load.
+constexpr int kBatch = 4;
 constexpr float kRescaleSlack = 8.f;  // log2 units
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMinTiles = 2;  // tiles per CTA, before more CTAs take part
 
-template <int D>
+template <int D, bool TWO>
 struct Cfg {
   static constexpr int kGroups = D == 128 ? 2 : 1;
-  static constexpr int kThreads = kGroups * kM + kProducers;
+  static constexpr bool kHalves = kGroups == 2 && !TWO;  // the groups share rows and split the tiles
+  // + a warpgroup of which one warp issues the MMAs and one stores the new rows
+  static constexpr int kThreads = kGroups * kM + kCopiers + 128;
+  // registers per thread of the softmax, copy and MMA warpgroups; they add up to the launch's
+  // (65536 / kThreads, a multiple of 8, per thread)
+  static constexpr int kRegsSoftmax = D == 128 ? 168 : 232, kRegsCopy = D == 128 ? 96 : 136,
+                       kRegsIssue = D == 128 ? 80 : 136;
+  static_assert(kGroups * kM * kRegsSoftmax + 128 * (kRegsCopy + kRegsIssue) ==
+                    kThreads * (65536 / kThreads / 8 * 8), "register split");
   static constexpr int kBlockBytes = kTT * 128;              // 64 tokens x 64 dimensions
   static constexpr int kTileBytes = D / 64 * kBlockBytes;    // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kTileBytes;         // K then V
-  static constexpr int kStages = D == 128 ? 6 : 3;
-  static constexpr int kAhead = D == 128 ? 3 : 1;            // newer tiles in flight behind a landed one
-  static constexpr int kSmem = 1024 + kStages * kStageBytes;
-  // tensor memory columns: Q (bf16 A operand), S / P, O of each group
-  static constexpr uint32_t kQ = 0, kQCols = D / 2;
-  static constexpr uint32_t kS = 128, kO = 256;
+  static constexpr int kQBytes = TWO ? kM * D * 2 : 0;       // Q of group 1
+  static constexpr int kStages = D == 128 ? (TWO ? 5 : 6) : 3;
+  static constexpr int kSmem = 1024 + kQBytes + kStages * kStageBytes;
+  // tensor memory columns: Q (A operand, bf16) of group 0 (of both), P of each group (A operand,
+  // bf16), S and O of each group (fp32)
+  static constexpr uint32_t kQ = 0, kP = D == 128 ? 64 : 192, kS = 128, kO = 256;
 };
 
 // What the tiles of one (sequence, KV head) walk over: list index j < n_ctx is context position
@@ -138,21 +152,19 @@ __device__ __forceinline__ float merge_weight(float m, float l, float M) {
 }
 __device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.f / l : (l == l ? 0.f : l); }
 
-// Workspace: [tiles in the line, CTAs per row group that share them][first tile of each pair]
-// [(m, l) of each partial row][O of each partial row].
+// Workspace: [where each CTA's tiles begin: pair (-1: none), tile][(m, l) of each partial row]
+// [O of each partial row].
 struct Work {
-  int64_t* head;
-  int64_t* first;  // [pairs + 1]
-  float2* ml;      // [2 * CTAs][rows]
-  float* o;        // [2 * CTAs][rows][D]
+  int2* at;    // [CTAs]
+  float2* ml;  // [2 * CTAs][rows]
+  float* o;    // [2 * CTAs][rows][D]
 };
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-__host__ __device__ inline Work work_of(void* ws, int64_t pairs, int64_t ctas, int64_t rows) {
+__host__ __device__ inline Work work_of(void* ws, int64_t ctas, int64_t rows) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   Work w;
-  w.head = reinterpret_cast<int64_t*>(p);
-  w.first = w.head + 2;
-  p += up256((pairs + 3) * 8);
+  w.at = reinterpret_cast<int2*>(p);
+  p += up256(ctas * sizeof(int2));
   w.ml = reinterpret_cast<float2*>(p);
   p += up256(2 * ctas * rows * sizeof(float2));
   w.o = reinterpret_cast<float*>(p);
@@ -178,34 +190,38 @@ inline Plan plan_tree(int n, int G, int d) {
 }
 
 template <int D, bool TWO>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
     tree_kernel(TreeArgs a, int row_groups, int slot_rows, long long limit) {
-  using C = Cfg<D>;
+  using C = Cfg<D, TWO>;
   constexpr int kGroups = C::kGroups;
-  constexpr bool kHalves = kGroups == 2 && !TWO;  // the groups share rows and split the tiles
+  constexpr bool kHalves = C::kHalves;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages];
-  __shared__ __align__(8) uint64_t s_bar[3 * kGroups];  // per group: S ready, P V done, drain
-  __shared__ uint16_t s_valid[C::kStages][kTT / 16];    // usable positions of a stage
+  // per group: S ready, P V done (commits), S read, P ready, Q ready (an arrival of each warp)
+  enum { kBarS, kBarO, kBarFree, kBarP, kBarQ, kBars };
+  __shared__ __align__(8) uint64_t s_bar[kBars * kGroups + 1];  // the last one: drain
+  __shared__ __align__(8) uint64_t s_valid[C::kStages];         // usable positions of a stage
+  // offset (elements, a multiple of 8) of each row in the caches, or in k_new / v_new with bit 0
+  // set; -1: not usable
+  __shared__ int64_t s_off[kCopiers / 32][kBatch * 16];
   __shared__ float2 s_ml[2][kM];
-  __shared__ uint32_t s_bad[kGroups][4];
+  __shared__ uint32_t s_bad[kGroups][4], s_keep[kGroups];
   __shared__ int64_t s_sum[C::kThreads / 32];
-  __shared__ int64_t s_begin, s_end;
+  __shared__ int64_t s_todo;
   __shared__ int s_pair, s_tile;
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring = (smem_u32(tree_smem) + 1023u) & ~1023u;
+  const uint32_t q_smem = (smem_u32(tree_smem) + 1023u) & ~1023u, ring = q_smem + C::kQBytes;
   const int pairs = a.batch * a.h_kv, G = a.h_q / a.h_kv, rows = a.n * G;
   const int rg = blockIdx.x % row_groups, cta = blockIdx.x / row_groups;
-  const int n_cta = gridDim.x / row_groups;
-  const Work ws = work_of(a.ws, pairs, gridDim.x, slot_rows);
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      tc::mbar_init(smem_u32(&s_full[i]), kProducers / 32);
+      tc::mbar_init(smem_u32(&s_full[i]), kCopiers + kCopiers / 32);
       tc::mbar_init(smem_u32(&s_empty[i]), TWO ? 2 : 1);
     }
-    for (int i = 0; i < 3 * kGroups; ++i) tc::mbar_init(smem_u32(&s_bar[i]), 1);
+    for (int i = 0; i < kBars * kGroups + 1; ++i)
+      tc::mbar_init(smem_u32(&s_bar[i]), i == kBars * kGroups || i % kBars < kBarFree ? 1 : 4);
     tc::fence_mbar_init();
   }
   if (warp == 0) {
@@ -231,25 +247,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (w < warp) before += s_sum[w];
       total += s_sum[w];
     }
-    const int64_t n_work = min((int64_t)n_cta, (total + kMinTiles - 1) / kMinTiles);
+    const int64_t n_cta = gridDim.x / row_groups;
+    const int64_t n_work = min(n_cta, (total + kMinTiles - 1) / kMinTiles);
     const int64_t begin = cta < n_work ? cta * total / n_work : total;
     const int64_t end = cta < n_work ? (cta + 1) * total / n_work : total;
-    if (tid == 0) {
-      s_begin = begin;
-      s_end = end;
-      if (blockIdx.x == 0) {
-        ws.head[0] = total;
-        ws.head[1] = n_work;
-        ws.first[pairs] = total;
-      }
-    }
-    for (int q = q0; q < q1; ++q) {
+    if (tid == 0) s_todo = end - begin;
+    int2* at = work_of(a.ws, gridDim.x, slot_rows).at + cta;
+    if (tid == 0 && rg == 0 && begin == end) *at = make_int2(-1, 0);
+    for (int q = q0; q < q1 && begin < end; ++q) {
       const int t = pair_of(a, q).tiles;
       if (begin >= before && begin < before + t) {
         s_pair = q;
         s_tile = (int)(begin - before);
+        if (rg == 0) *at = make_int2(q, (int)(begin - before));
       }
-      if (blockIdx.x == 0) ws.first[q] = before;
       before += t;
     }
   }
@@ -258,149 +269,292 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   tc::fence_after_sync();
   pdl_trigger();
   const uint32_t tmem = s_tmem;
-  const int64_t todo = s_end - s_begin;
+  const int64_t todo = s_todo;
   int pair = s_pair, t0 = s_tile;
   bool fail = false;
 
-  if (warp >= kGroups * 4) {
-    // ---- producers: 16 rows of a tile per warp ---------------------------------------------------
-    const int pw = warp - kGroups * 4;
-    constexpr int kChunks = D / 8;                 // 16-byte chunks per row
-    constexpr int kRowsPer = 32 / kChunks ? 32 / kChunks : 1;  // rows per warp copy
-    const int shift = 31 - __clz(a.page_size), max_len = a.max_pages * a.page_size;
-    // cursor over (pair, tile), one tile ahead of the copies
-    Pair p = {};
-    Tree tree = {};
-    int cur = t0, at_pair = pair;
-    int64_t left = todo;
-    if (left > 0) {
-      p = pair_of(a, at_pair);
-      tree = tree_of(a, p.b, lane, pw == 0 && rg == 0);
-      if (pw == 0 && lane == 0 && a.seq_lens[p.b] != p.L) raise_flag(4u);
-    }
-    struct Row {
-      const uint16_t* k;  // null: not usable
-      const uint16_t* v;
-      int64_t store;      // cache offset a new row goes to, or -1
-    };
-    // the source of row (16 pw + lane) of the cursor's tile (lanes 0-15); the cursor moves on
-    auto next_row = [&]() {
-      Row r = {nullptr, nullptr, -1};
-      const uint64_t used0 = __ballot_sync(kAll, tree.see[0] != 0ull);
-      const uint64_t used1 = __ballot_sync(kAll, tree.see[1] != 0ull);
-      const uint64_t used = used0 | (used1 << 32);
-      const int j = cur * kTT + pw * 16 + lane;
-      int node = -1, pos = -1;
-      bool want = false;
-      if (lane < 16) {
-        if (j < p.n_ctx) {
-          pos = a.idx ? a.idx[(int64_t)at_pair * a.budget + j] : p.lo + j;
-          want = true;
-        } else if (j - p.n_ctx < a.n && ((used >> (j - p.n_ctx)) & 1ull)) {
-          node = j - p.n_ctx;
-          pos = p.L + node;
-          want = true;
-        }
-      }
-      if (want) {
-        if (pos < 0 || pos >= max_len) {
-          raise_flag(2u);
+  if (warp >= kGroups * 4 + 4) {
+    tc::regs_dec<C::kRegsIssue>();
+    if (warp == kGroups * 4 + 4) {
+      // ---- MMA issue: all lanes run the loop, one issues -------------------------------------------
+      // Items in order: (tile, group) with rows of their own, tiles of alternating groups otherwise.
+      // The S of a group's next item goes before the P V of this one.
+      constexpr uint32_t kIdescS = tc::idesc_bf16(kM, kTT, false);
+      constexpr uint32_t kIdescO = tc::idesc_bf16(kM, D, true);
+      constexpr int kStride = kHalves ? 2 : 1;  // tiles from one item of a group to its next
+      const uint32_t on = tc::elect_one();
+      uint32_t n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_q = 0;  // S, P V and segments so far
+      auto bar = [&](int g, int which) { return smem_u32(&s_bar[kBars * g + which]); };
+      auto wait = [&](uint32_t b, uint32_t parity) {  // (the whole warp agrees)
+        if (!fail) fail = __any_sync(kAll, !tc::mbar_wait(b, parity, limit));
+      };
+      auto stage_of = [&](int64_t k) { return ring + (uint32_t)(k % C::kStages) * C::kStageBytes; };
+      auto issue_s = [&](int g, int64_t k) {
+        if (n_s[g] > 0) wait(bar(g, kBarFree), (n_s[g] - 1) & 1);
+        ++n_s[g];
+        wait(smem_u32(&s_full[k % C::kStages]), (uint32_t)((k / C::kStages) & 1));
+        if (fail) return;
+        // the rows came by cp.async (generic proxy); the tensor cores read through the async proxy
+        tc::fence_proxy_async_smem();
+        tc::fence_after_sync();
+        const uint32_t ts = tmem + C::kS + g * kTT;
+        const uint64_t b0 = tc::sw128_desc(stage_of(k), 16, 1024);
+        if (TWO && g == 1) {
+          const uint64_t a0 = tc::sw128_desc(q_smem, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ss_warp(on, ts, a0 + (uint64_t)(((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4),
+                            b0 + (uint64_t)(((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4),
+                            kIdescS, kk > 0);
         } else {
-          const int pg = a.block_table[(int64_t)p.b * a.max_pages + (pos >> shift)];
-          if (pg < 0 || (int64_t)pg >= a.num_pages) {
-            raise_flag(1u);
-          } else {
-            const int64_t off = (int64_t)pg * a.page_stride +
-                                (int64_t)(pos & (a.page_size - 1)) * a.slot_stride +
-                                (int64_t)p.h * a.head_stride;
-            if (node >= 0 && a.k_new) {
-              const int64_t src = (((int64_t)p.b * a.n + node) * a.h_kv + p.h) * D;
-              r.k = a.k_new + src;
-              r.v = a.v_new + src;
-              r.store = off;
-            } else {
-              r.k = a.k_cache + off;
-              r.v = a.v_cache + off;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ts_warp(on, ts, tmem + C::kQ + kk * 8,
+                            b0 + (uint64_t)(((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4),
+                            kIdescS, kk > 0);
+        }
+        tc::mma_commit_warp(on, bar(g, kBarS));
+      };
+      int64_t k0 = 0;
+      while (k0 < todo) {
+        const int tiles = pair_of(a, pair).tiles;
+        const int n = (int)min((int64_t)tiles - t0, todo - k0);  // tiles of the segment
+        for (int g = 0; g < kGroups; ++g) {
+          if (kHalves ? g == 0 : true) wait(bar(g, kBarQ), n_q & 1);
+          if (!kHalves || g < n) issue_s(g, k0 + (kHalves ? g : 0));
+        }
+        ++n_q;
+        for (int i = 0; i < n; ++i) {
+#pragma unroll
+          for (int gg = 0; gg < (kHalves ? 1 : kGroups); ++gg) {
+            const int g = kHalves ? i & 1 : gg;
+            const int64_t k = k0 + i;
+            if (i + kStride < n) issue_s(g, k + kStride);
+            wait(bar(g, kBarP), n_p[g] & 1);
+            ++n_p[g];
+            if (fail) continue;
+            tc::fence_after_sync();
+            const uint32_t tp = tmem + C::kP + g * (kTT / 2), to = tmem + C::kO + g * D;
+            const uint64_t b0 = tc::sw128_desc(stage_of(k) + C::kTileBytes, C::kBlockBytes, 1024);
+            const bool more = *(volatile uint32_t*)&s_keep[g] != 0u;
+#pragma unroll
+            for (int kk = 0; kk < kTT / 16; ++kk)
+              tc::mma_ts_warp(on, to, tp + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
+                              more || kk > 0);
+            tc::mma_commit_warp(on, bar(g, kBarO));
+            tc::mma_commit_warp(on, smem_u32(&s_empty[k % C::kStages]));
+          }
+        }
+        k0 += n;
+        t0 = 0;
+        ++pair;
+      }
+      // everything issued has completed before the tensor memory is freed
+      tc::mma_commit_warp(on, smem_u32(&s_bar[kBars * kGroups]));
+      if (!tc::mbar_wait(smem_u32(&s_bar[kBars * kGroups]), 0)) fail = true;
+    } else if (warp == kGroups * 4 + 5 && rg == 0) {
+      // ---- bad lengths and parents are reported, the new nodes' rows written to the cache -----------
+      const int max_len = a.max_pages * a.page_size;
+      for (int64_t k0 = 0; k0 < todo;) {
+        const Pair p = pair_of(a, pair);
+        const int t1 = (int)min((int64_t)p.tiles, t0 + todo - k0);
+        if (lane == 0 && a.seq_lens[p.b] != p.L) raise_flag(4u);
+        const Tree tree = tree_of(a, p.b, lane, true);
+        if (a.k_new) {
+          int64_t to[2];  // of nodes lane and lane + 32
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int node = lane + 32 * u, j = p.n_ctx + node, pos = p.L + node;
+            to[u] = -1;
+            if (tree.see[u] && j >= t0 * kTT && j < t1 * kTT && pos < max_len) {
+              const int pg = a.block_table[(int64_t)p.b * a.max_pages + pos / a.page_size];
+              if (pg >= 0 && (int64_t)pg < a.num_pages)
+                to[u] = (int64_t)pg * a.page_stride + (int64_t)(pos % a.page_size) * a.slot_stride +
+                        (int64_t)p.h * a.head_stride;
+            }
+          }
+          // 4 rows at a time; lanes 0-15 K and 16-31 V at d = 128, chunk `lane` of both at d = 256
+          const int c = D == 128 ? lane & 15 : lane;
+          const bool is_v = D == 128 && lane >= 16;
+#pragma unroll 1
+          for (int i0 = 0; i0 < a.n; i0 += 4) {
+            int64_t dst[4];
+            uint4 x[4], y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int i = i0 + u;
+              const int64_t d0 = __shfl_sync(kAll, to[0], i & 31), d1 = __shfl_sync(kAll, to[1], i & 31);
+              dst[u] = i < 32 ? d0 : d1;
+              const int64_t src = (((int64_t)p.b * a.n + i) * a.h_kv + p.h) * D + c * 8;
+              if (dst[u] >= 0) {
+                x[u] = *reinterpret_cast<const uint4*>((is_v ? a.v_new : a.k_new) + src);
+                if (D == 256) y[u] = *reinterpret_cast<const uint4*>(a.v_new + src);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (dst[u] < 0) continue;
+              *reinterpret_cast<uint4*>((is_v ? a.v_cache : a.k_cache) + dst[u] + c * 8) = x[u];
+              if (D == 256) *reinterpret_cast<uint4*>(a.v_cache + dst[u] + c * 8) = y[u];
             }
           }
         }
-      }
-      if (--left > 0 && ++cur == p.tiles) {
-        p = pair_of(a, ++at_pair);
-        cur = 0;
-        tree = tree_of(a, p.b, lane, pw == 0 && rg == 0);
-        if (pw == 0 && lane == 0 && a.seq_lens[p.b] != p.L) raise_flag(4u);
-      }
-      return r;
-    };
-    Row row = {nullptr, nullptr, -1};
-    if (todo > 0) row = next_row();
-    const int c = lane % kChunks;
-    for (int64_t k = 0; k < todo; ++k) {
-      const int st = (int)(k % C::kStages);
-      const Row now = row;
-      if (k + 1 < todo) row = next_row();
-      if (!fail) fail = !tc::mbar_wait(smem_u32(&s_empty[st]), (uint32_t)((k / C::kStages) & 1) ^ 1u, limit);
-      const unsigned ok = __ballot_sync(kAll, now.k != nullptr);
-      if (lane == 0) s_valid[st][pw] = (uint16_t)ok;
-      const uint32_t stage = ring + st * C::kStageBytes;
-      bool any_new = false;
-#pragma unroll
-      for (int it = 0; it < 16 / kRowsPer; ++it) {
-        const int u = it * kRowsPer + (kRowsPer == 2 ? lane >> 4 : 0);
-        const uint16_t* ks = reinterpret_cast<const uint16_t*>(__shfl_sync(kAll, (unsigned long long)now.k, u));
-        const uint16_t* vs = reinterpret_cast<const uint16_t*>(__shfl_sync(kAll, (unsigned long long)now.v, u));
-        const int tr = pw * 16 + u;
-        const uint32_t dst = stage + (c >> 3) * C::kBlockBytes + tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
-        cp_async16(dst, (ks ? ks : a.k_cache) + c * 8, ks ? 16 : 0);
-        cp_async16(dst + C::kTileBytes, (vs ? vs : a.v_cache) + c * 8, vs ? 16 : 0);
-      }
-      cp_async_commit();
-      any_new = __any_sync(kAll, now.store >= 0);
-      if (any_new && rg == 0) {  // the new nodes' rows into the cache
-#pragma unroll 1
-        for (int u = 0; u < 16; ++u) {
-          const int64_t to = __shfl_sync(kAll, now.store, u);
-          const uint4* ks = reinterpret_cast<const uint4*>(__shfl_sync(kAll, (unsigned long long)now.k, u));
-          const uint4* vs = reinterpret_cast<const uint4*>(__shfl_sync(kAll, (unsigned long long)now.v, u));
-          if (to >= 0 && lane < kChunks) {
-            *(reinterpret_cast<uint4*>(a.k_cache + to) + lane) = ks[lane];
-            *(reinterpret_cast<uint4*>(a.v_cache + to) + lane) = vs[lane];
-          }
-        }
-      }
-      if (k >= C::kAhead) {
-        cp_async_wait<C::kAhead>();
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(smem_u32(&s_full[(k - C::kAhead) % C::kStages]));
+        k0 += t1 - t0;
+        t0 = 0;
+        ++pair;
       }
     }
-    cp_async_wait<0>();
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0)
-      for (int64_t k = max((int64_t)0, todo - C::kAhead); k < todo; ++k)
-        tc::mbar_arrive(smem_u32(&s_full[k % C::kStages]));
+  } else if (warp >= kGroups * 4) {
+    // ---- row copies: 16 rows of a tile per warp -----------------------------------------------------
+    tc::regs_dec<C::kRegsCopy>();
+    const int pw = warp - kGroups * 4;
+    constexpr int kChunks = D / 8;                             // 16-byte chunks per row
+    constexpr int kRowsPer = 32 / kChunks ? 32 / kChunks : 1;  // rows per copy instruction
+    constexpr int kIters = 16 / kRowsPer, kUnroll = 8;
+    const int c = lane % kChunks, half = kRowsPer == 2 ? lane >> 4 : 0;
+    const int shift = 31 - __clz(a.page_size), max_len = a.max_pages * a.page_size;
+    // Offsets of a batch (tiles t .. t + n - 1 of one pair): this lane's rows are row
+    // 16 pw + lane % 16 of tiles t + lane / 16 and t + 2 + lane / 16. The positions (index set) of
+    // the batch after next and the pages of the next one are in flight while a batch is copied.
+    constexpr int kNone = INT_MIN;
+    struct Batch {
+      int b, h, n_ctx, t, n;
+    };
+    Batch next = {};
+    int64_t left = todo;
+    int tiles = 0, L = 0, lo = 0;
+    auto advance = [&]() {  // the next batch of the line; n = 0 behind its end
+      if (left <= 0) {
+        next.n = 0;
+        return;
+      }
+      next.t += next.n;
+      if (next.t == tiles) {  // (also at the start, with tiles = t = 0)
+        const Pair p = pair_of(a, pair);
+        next.b = p.b; next.h = p.h; next.n_ctx = p.n_ctx;
+        next.t = t0;
+        tiles = p.tiles; L = p.L; lo = p.lo;
+        t0 = 0;
+        ++pair;
+      }
+      next.n = (int)min(min((int64_t)kBatch, left), (int64_t)(tiles - next.t));
+      left -= next.n;
+    };
+    auto position = [&](int x) {  // of row x of `next`; kNone: no token there
+      const int i = 2 * x + (lane >> 4);
+      const int j = (next.t + i) * kTT + 16 * pw + (lane & 15), node = j - next.n_ctx;
+      if (i >= next.n || node >= a.n) return kNone;
+      if (node < 0)
+        return a.idx ? max(a.idx[((int64_t)next.b * a.h_kv + next.h) * a.budget + j], -1) : lo + j;
+      const int par = a.parents[(int64_t)next.b * a.n + node];
+      return par >= -1 && par < node ? L + node : kNone;
+    };
+    auto page = [&](int b, int pos) {
+      return pos >= 0 && pos < max_len ? a.block_table[(int64_t)b * a.max_pages + (pos >> shift)] : -1;
+    };
+    advance();
+    Batch now = next;
+    int pos0 = position(0), pos1 = position(1);
+    int pg0 = page(now.b, pos0), pg1 = page(now.b, pos1);
+    advance();
+    int npos0 = position(0), npos1 = position(1);
+    int st = 0;
+    uint32_t lap = 0;
+    while (now.n > 0) {
+      const int n = now.n;
+      uint32_t bad = 0u;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int ps = x ? pos1 : pos0, pg = x ? pg1 : pg0;
+        int64_t off = -1;
+        if (ps != kNone) {
+          if (ps < 0 || ps >= max_len) {
+            bad |= 2u;
+          } else if (pg < 0 || (int64_t)pg >= a.num_pages) {
+            bad |= 1u;
+          } else {
+            const int node = (now.t + 2 * x + (lane >> 4)) * kTT + 16 * pw + (lane & 15) - now.n_ctx;
+            if (node >= 0 && a.k_new)
+              off = ((((int64_t)now.b * a.n + node) * a.h_kv + now.h) * D) | 1;
+            else
+              off = (int64_t)pg * a.page_stride + (int64_t)(ps & (a.page_size - 1)) * a.slot_stride +
+                    (int64_t)now.h * a.head_stride;
+          }
+        }
+        s_off[pw][32 * x + lane] = off;
+      }
+      if (bad) raise_flag(bad);
+      __syncwarp();
+      now = next;
+      pos0 = npos0;
+      pos1 = npos1;
+      pg0 = page(now.b, pos0);
+      pg1 = page(now.b, pos1);
+      advance();
+      npos0 = position(0);
+      npos1 = position(1);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int64_t* offs = &s_off[pw][16 * i];
+        if (!fail) fail = !tc::mbar_wait(smem_u32(&s_empty[st]), (lap & 1) ^ 1u, limit);
+        const uint32_t stage = ring + st * C::kStageBytes + (c >> 3) * C::kBlockBytes;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kIters; i0 += kUnroll) {
+          int64_t off[kUnroll];  // (all of them first: the copies are not reordered with loads)
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) off[u] = offs[(i0 + u) * kRowsPer + half];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) {
+            const int64_t at = (off[u] >= 0 ? off[u] & ~1ll : 0) + c * 8;
+            const bool fresh = off[u] >= 0 && (off[u] & 1);
+            const int tr = pw * 16 + (i0 + u) * kRowsPer + half, n_bytes = off[u] >= 0 ? 16 : 0;
+            const uint32_t dst = stage + tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
+            cp_async16(dst, (fresh ? a.k_new : a.k_cache) + at, n_bytes);
+            cp_async16(dst + C::kTileBytes, (fresh ? a.v_new : a.v_cache) + at, n_bytes);
+          }
+        }
+        const unsigned ok = __ballot_sync(kAll, offs[lane & 15] >= 0);
+        if (lane == 0) reinterpret_cast<uint16_t*>(&s_valid[st])[pw] = (uint16_t)ok;
+        tc::mbar_arrive_cp_async(smem_u32(&s_full[st]));
+        if (lane == 0) tc::mbar_arrive(smem_u32(&s_full[st]));  // (s_valid is written)
+        if (++st == C::kStages) {
+          st = 0;
+          ++lap;
+        }
+      }
+      __syncwarp();  // the offsets have been read
+    }
+    cp_async_wait_all();
   } else {
     // ---- softmax groups ----------------------------------------------------------------------------
+    tc::regs_inc<C::kRegsSoftmax>();
     const int g = warp >> 2, gt = tid & (kM - 1);  // group, thread of the group = tensor-memory lane
     const int gbar = 1 + g;                        // the group's named barrier; 3: both groups
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tq = tmem + C::kQ + g * C::kQCols, ts = tmem + C::kS + g * kTT,
-                   to = tmem + C::kO + g * D;
-    const uint32_t bar_s = smem_u32(&s_bar[3 * g]), bar_o = smem_u32(&s_bar[3 * g + 1]),
-                   bar_d = smem_u32(&s_bar[3 * g + 2]);
-    constexpr uint32_t kIdescS = tc::idesc_bf16(kM, kTT, false);
-    constexpr uint32_t kIdescO = tc::idesc_bf16(kM, D, true);
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
+    const uint32_t ts = tl + C::kS + g * kTT, tp = tl + C::kP + g * (kTT / 2), to = tl + C::kO + g * D;
+    auto bar = [&](int which) { return smem_u32(&s_bar[kBars * g + which]); };
+    // this warp has done its part: its tensor-memory accesses are complete before the arrival
+    auto arrive = [&](int which) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(which));
+    };
     // (a negative scale is a negated Q; a zero scale must not turn the mask's -inf into NaN)
     const float scale_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     const int r = rg * (TWO ? 2 * kM : kM) + (TWO ? g * kM : 0) + gt;  // query row of this thread
     const int node = min(r / G, kTreeMaxNodes - 1);
-    uint32_t n_s = 0, n_o = 0;  // phases of bar_s and bar_o so far
-    int64_t k0 = 0;             // line index (within the CTA) of the segment's first tile
+    uint32_t n_t = 0;  // tiles of this group so far (phases of its barriers)
+    int64_t k0 = 0;    // line index (within the CTA) of the segment's first tile
     while (k0 < todo) {
+      // Q: this thread's row (on its way to L1 while the pair and the tree are resolved)
+      const bool q_tmem = !TWO || g == 0, q_mine = !kHalves || g == 0;
+      const int pb = pair / a.h_kv;
+      const int64_t q_off = r < rows ? (((int64_t)pb * a.n + node) * a.h_q + (int64_t)(pair - pb * a.h_kv) * G + r % G) * D : 0;
+      const uint4* qrow = reinterpret_cast<const uint4*>(a.q + q_off);
+      if (q_mine)
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) prefetch_l1(qrow + 8 * u);
       const Pair p = pair_of(a, pair);
       const int t1 = (int)min((int64_t)p.tiles, t0 + todo - k0);
       const Tree tree = tree_of(a, p.b, lane, false);
@@ -413,52 +567,50 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         lo = min(max(0, p.L + depth - a.window + 1) - p.lo, p.n_ctx);
         for (int x = depth + 1 - a.window; x > 0; --x) see &= see - 1;  // (ancestors: ascending depth)
       }
-      // Q: this thread's row into its lane
-      {
-        const int64_t qo = (((int64_t)p.b * a.n + node) * a.h_q + (int64_t)p.h * G + r % G) * D;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (used ? qo : 0));
-#pragma unroll
+      if (q_mine) {
+#pragma unroll(D == 128 ? 2 : 1)
         for (int c = 0; c < D / 64; ++c) {
           uint32_t v[32];
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const uint4 x = used ? __ldg(src + c * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
-            v[4 * u] = x.x ^ flip;
-            v[4 * u + 1] = x.y ^ flip;
-            v[4 * u + 2] = x.z ^ flip;
-            v[4 * u + 3] = x.w ^ flip;
+            const uint4 x = qrow[8 * c + u];
+            v[4 * u] = used ? x.x ^ flip : 0u;
+            v[4 * u + 1] = used ? x.y ^ flip : 0u;
+            v[4 * u + 2] = used ? x.z ^ flip : 0u;
+            v[4 * u + 3] = used ? x.w ^ flip : 0u;
           }
-          tc::tmem_st32(tq + lane_base + 32 * c, v);
+          if (q_tmem) {
+            tc::tmem_st32(tl + C::kQ + 32 * c, v);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              st_shared_v4(q_smem + c * kM * 128 + gt * 128 + ((u ^ (gt & 7)) << 4), v[4 * u],
+                           v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+          }
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        tc::bar_sync(gbar, kM);
+        if (q_tmem) tc::tmem_wait_st();
+        else tc::fence_proxy_async_smem();
+        arrive(kBarQ);
       }
       float m_ref = -INFINITY, l = 0.f;
       bool have_o = false;
       const bool active = __any_sync(kAll, used);  // a warp of padding rows only keeps the barriers
+      int st = (int)((k0 + (kHalves ? g : 0)) % C::kStages);
+      uint32_t lap = (uint32_t)((k0 + (kHalves ? g : 0)) / C::kStages);
+#pragma unroll 1
       for (int t = t0 + (kHalves ? g : 0); t < t1; t += kHalves ? 2 : 1) {
-        const int64_t k = k0 + (t - t0);
-        const int st = (int)(k % C::kStages);
         const uint32_t stage = ring + st * C::kStageBytes;
-        if (!fail) fail = !tc::mbar_wait(smem_u32(&s_full[st]), (uint32_t)((k / C::kStages) & 1), limit);
-        if (gt == 0 && !fail) {
-          // (P of the previous tile lies over S: its P V has to be done)
-          if (n_o > 0) fail = !tc::mbar_wait(bar_o, (n_o - 1) & 1, limit);
-          if (!fail) {
-            tc::fence_after_sync();
-            const uint64_t b0 = tc::sw128_desc(stage, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma_ts(ts, tq + kk * 8,
-                         b0 + (uint64_t)(((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4), kIdescS,
-                         kk > 0);
-            tc::mma_commit(bar_s);
-          }
+        if (!fail) fail = !tc::mbar_wait(bar(kBarS), n_t & 1, limit);
+        tc::fence_after_sync();
+        uint32_t s0[32], s1[32];
+        if (active) {
+          tc::tmem_ld32(ts, s0);
+          tc::tmem_ld32(ts + 32, s1);
         }
+        // (S is there, so the rows are: this wait only makes s_valid visible)
+        if (!fail) fail = !tc::mbar_wait(smem_u32(&s_full[st]), lap & 1, limit);
         // the list indexes of this tile that the row sees
-        const uint16_t* vp = s_valid[st];
-        uint64_t see_t = (uint64_t)vp[0] | ((uint64_t)vp[1] << 16) | ((uint64_t)vp[2] << 32) | ((uint64_t)vp[3] << 48);
+        uint64_t see_t = s_valid[st];
         const int j0 = t * kTT, c_left = p.n_ctx - j0;  // context positions from here on
         if (c_left < kTT) {
           const uint64_t ctx = c_left > 0 ? (1ull << c_left) - 1ull : 0ull;
@@ -469,66 +621,69 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (!used) see_t = ~0ull;  // (its row is discarded)
         // uniform over the CTA: some row may mask a position that is in the tile
         const bool special = c_left < kTT || (a.window > 0 && t == 0);
-
-        if (!fail) fail = !tc::mbar_wait(bar_s, n_s & 1, limit);
-        ++n_s;
-        tc::fence_after_sync();
-        uint32_t ph[32];
+        if (active) tc::tmem_wait_ld();
+        arrive(kBarFree);
         if (active) {
-          uint32_t s0[32], s1[32];
-          tc::tmem_ld32(ts + lane_base, s0);
-          tc::tmem_ld32(ts + lane_base + 32, s1);
-          tc::tmem_wait_ld();
-          float x[kTT];
-          if (__all_sync(kAll, see_t == ~0ull)) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              x[j] = __uint_as_float(s0[j]);
-              x[j + 32] = __uint_as_float(s1[j]);
-            }
-          } else {
+          if (!__all_sync(kAll, see_t == ~0ull)) {
             const uint32_t lo32 = (uint32_t)see_t, hi32 = (uint32_t)(see_t >> 32);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              x[j] = ((lo32 >> j) & 1u) ? __uint_as_float(s0[j]) : -INFINITY;
-              x[j + 32] = ((hi32 >> j) & 1u) ? __uint_as_float(s1[j]) : -INFINITY;
+              if (!((lo32 >> j) & 1u)) s0[j] = 0xFF800000u;  // -inf
+              if (!((hi32 >> j) & 1u)) s1[j] = 0xFF800000u;
             }
           }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
+          float mx[4];
 #pragma unroll
-          for (int j = 4; j < kTT; j += 4)
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(__uint_as_float(s0[u]), __uint_as_float(s1[u]));
 #pragma unroll
-            for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[j + u]);
+          for (int j = 4; j < 32; j += 4)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              mx[u] = fmaxf(mx[u], fmaxf(__uint_as_float(s0[j + u]), __uint_as_float(s1[j + u])));
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
           // lazy rescale: weights are relative to m_ref, which moves only when the row's maximum
           // exceeds it by more than the slack (weights stay <= 2^8)
           const bool grow = mt > m_ref + kRescaleSlack;
           const float m_new = grow ? mt : m_ref;
           const float corr = grow && m_ref != -INFINITY ? fast_exp2(m_ref - m_new) : 1.f;
+          // P V of the group's previous tile: done with P and O
+          if (n_t > 0 && !fail) fail = !tc::mbar_wait(bar(kBarO), (n_t - 1) & 1, limit);
+          tc::fence_after_sync();
           if (have_o && __any_sync(kAll, corr != 1.f)) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
-              tc::tmem_ld32(to + lane_base + 32 * c, o);
+              tc::tmem_ld32(to + 32 * c, o);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-              tc::tmem_st32(to + lane_base + 32 * c, o);
+              tc::tmem_st32(to + 32 * c, o);
             }
           }
           m_ref = m_new;
           const float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
           float sum[2] = {0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p0 = fast_exp2(fmaf(x[2 * j], scale_log2, -m_sub));
-            const float p1 = fast_exp2(fmaf(x[2 * j + 1], scale_log2, -m_sub));
-            sum[0] += p0;
-            sum[1] += p1;
-            ph[j] = pack_bf16x2(p0, p1);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t ph[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float x0 = __uint_as_float(h ? s1[2 * j] : s0[2 * j]);
+              const float x1 = __uint_as_float(h ? s1[2 * j + 1] : s0[2 * j + 1]);
+              const float p0 = fast_exp2(fmaf(x0, scale_log2, -m_sub));
+              const float p1 = fast_exp2(fmaf(x1, scale_log2, -m_sub));
+              sum[0] += p0;
+              sum[1] += p1;
+              ph[j] = pack_bf16x2(p0, p1);
+            }
+            tc::tmem_st16(tp + 16 * h, ph);
           }
           l = l * corr + (sum[0] + sum[1]);
-          tc::tmem_st32(ts + lane_base, ph);
+          tc::tmem_wait_st();
+        } else {
+          // (keeps this warp's arrivals in step: P of the previous tile has been taken)
+          if (n_t > 0 && !fail) fail = !tc::mbar_wait(bar(kBarO), (n_t - 1) & 1, limit);
+          tc::fence_after_sync();
         }
         bool keep_o = have_o;
         if (special) {
@@ -540,16 +695,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             return vrow + (c >> 3) * C::kBlockBytes + (((c & 7) ^ ((gt >> 1) & 7)) << 4);
           };
           auto odd = [](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
-          auto ld = [](uint32_t at) {
-            uint4 y;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at) : "memory");
-            return y;
-          };
           bool mine = false;
 #pragma unroll
           for (int q = 0; q < kPer; ++q) {
-            const uint4 y = ld(chunk(q));
+            const uint4 y = ld_shared_v4(chunk(q));
             mine |= odd(y.x) | odd(y.y) | odd(y.z) | odd(y.w);
           }
           const int vbar = TWO ? 3 : gbar, vthreads = TWO ? 2 * kM : kM;
@@ -558,15 +707,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (lane == 0) s_bad[g][warp & 3] = two;  // bit 2 i (+ 1): token 16 w + i
             tc::bar_sync(gbar, kM);
             // add p v of the non-finite elements to the rows that see them (O = 0 first)
-            tc::tmem_wait_st();
             uint32_t pl[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) pl[j] = ph[j];
+            tc::tmem_ld32(tp, pl);
+            tc::tmem_wait_ld();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               if (have_o) {
-                tc::tmem_ld32(to + lane_base + 32 * c, o);
+                tc::tmem_ld32(to + 32 * c, o);
                 tc::tmem_wait_ld();
               } else {
 #pragma unroll
@@ -581,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   const int cc = 4 * c + q;
-                  const uint4 y = ld(stage + C::kTileBytes + (cc >> 3) * C::kBlockBytes + j * 128 +
+                  const uint4 y = ld_shared_v4(stage + C::kTileBytes + (cc >> 3) * C::kBlockBytes + j * 128 +
                                      (((cc & 7) ^ (j & 7)) << 4));
                   const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -596,48 +744,45 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                   }
                 }
               }
-              tc::tmem_st32(to + lane_base + 32 * c, o);
+              tc::tmem_st32(to + 32 * c, o);
             }
             keep_o = true;
             tc::bar_sync(vbar, vthreads);  // everyone has read V
             if (!TWO || g == 0) {          // clear the elements for the MMA
 #pragma unroll 1
               for (int q = 0; q < kPer; ++q) {
-                const uint4 y = ld(chunk(q));
+                const uint4 y = ld_shared_v4(chunk(q));
                 uint32_t yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   if ((yw[e] & 0x7F80u) == 0x7F80u) yw[e] &= 0xFFFF0000u;
                   if ((yw[e] & 0x7F800000u) == 0x7F800000u) yw[e] &= 0x0000FFFFu;
                 }
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(q)), "r"(yw[0]),
-                             "r"(yw[1]), "r"(yw[2]), "r"(yw[3]) : "memory");
+                st_shared_v4(chunk(q), yw[0], yw[1], yw[2], yw[3]);
               }
               tc::fence_proxy_async_smem();
             }
             if (TWO) tc::bar_sync(vbar, vthreads);
           }
         }
+        // (thread 0 of the group also says whether P V adds to O: the same for all its tiles but the
+        // first, and but for the slow path above)
+        if (gt == 0) *(volatile uint32_t*)&s_keep[g] = keep_o;
         tc::tmem_wait_st();
-        tc::fence_before_sync();
-        tc::bar_sync(gbar, kM);
-        if (gt == 0 && !fail) {
-          tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < kTT / 16; ++kk)
-            tc::mma_ts(to, ts + kk * 8,
-                       tc::sw128_desc(stage + C::kTileBytes + kk * 16 * 128, C::kBlockBytes, 1024),
-                       kIdescO, keep_o || kk > 0);
-          tc::mma_commit(bar_o);
-          tc::mma_commit(smem_u32(&s_empty[st]));
-        }
-        ++n_o;
+        arrive(kBarP);
         have_o = true;
+        ++n_t;
+        st += kHalves ? 2 : 1;
+        if (st >= C::kStages) {
+          st -= C::kStages;
+          ++lap;
+        }
       }
-      if (have_o && !fail) fail = !tc::mbar_wait(bar_o, (n_o - 1) & 1, limit);
+      if (have_o && !fail) fail = !tc::mbar_wait(bar(kBarO), (n_t - 1) & 1, limit);
       tc::fence_after_sync();
 
       // ---- the segment's rows: into the output when the pair is whole, else into a partial slot
+      const Work ws = work_of(a.ws, gridDim.x, slot_rows);
       const bool whole = t0 == 0 && t1 == p.tiles;
       if (!used) {
         m_ref = -INFINITY;
@@ -664,13 +809,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int slot = 2 * blockIdx.x + (k0 > 0 ? 1 : 0), lr = (TWO ? g * kM : 0) + gt;
       const int64_t prow = (int64_t)slot * slot_rows + lr;
       if (!whole && r < rows && (!kHalves || g == 0)) ws.ml[prow] = make_float2(m_ref, l);
-      uint16_t* orow = a.out + (((int64_t)p.b * a.n + node) * a.h_q + (int64_t)p.h * G + r % G) * D;
+      uint16_t* orow = a.out + q_off;
       constexpr int kPart = kHalves ? D / 64 : D / 32;  // 32-column pieces written by this group
 #pragma unroll 1
       for (int c = (kHalves ? g * kPart : 0); c < (kHalves ? g * kPart : 0) + kPart; ++c) {
         uint32_t o[32];
         if (have_o) {
-          tc::tmem_ld32(to + lane_base + 32 * c, o);
+          tc::tmem_ld32(to + 32 * c, o);
           tc::tmem_wait_ld();
         }
 #pragma unroll
@@ -678,7 +823,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (kHalves) {
           if (__any_sync(kAll, other)) {
             uint32_t y[32];
-            tc::tmem_ld32(tmem + C::kO + (g ^ 1) * D + lane_base + 32 * c, y);
+            tc::tmem_ld32(tl + C::kO + (g ^ 1) * D + 32 * c, y);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -710,11 +855,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       t0 = 0;
       ++pair;
     }
-    // everything this group issued has completed before the tensor memory is freed
-    if (gt == 0) {
-      tc::mma_commit(bar_d);
-      if (!tc::mbar_wait(bar_d, 0)) fail = true;
-    }
   }
   if (fail) raise_flag(JSSA_DEVERR_TIMEOUT);
   tc::fence_before_sync();
@@ -725,95 +865,121 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
 }
 
-// Merge of the pairs that several CTAs share: one warp per query row,
+// Merge of the pairs that several CTAs share,
 //   M = max m_i,  w_i = 2^(m_i - M),  out = sum w_i O_i / sum w_i l_i.
-constexpr int kMergeWarps = 8;
+// Block (x, y): the pair in whose middle CTA x begins, if it is the first such CTA, and 32 of its
+// rows, 4 per warp (their loads in flight together).
+constexpr int kMergeWarps = 8, kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     merge_kernel(TreeArgs a, int row_groups, int group_rows, int slot_rows, int ctas) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int pair = blockIdx.x / row_groups, rg = blockIdx.x % row_groups;
-  const int pairs = a.batch * a.h_kv, G = a.h_q / a.h_kv;
-  const Work ws = work_of(a.ws, pairs, ctas, slot_rows);
+  const int x = blockIdx.x / row_groups + 1, rg = blockIdx.x % row_groups, n_cta = ctas / row_groups;
+  const Work ws = work_of(a.ws, ctas, slot_rows);
   pdl_wait();
-  const int64_t total = ws.head[0], n = ws.head[1], s0 = ws.first[pair], s1 = ws.first[pair + 1];
-  // CTA c covers tiles [c total / n, (c + 1) total / n): the one that holds tile t
-  auto holder = [&](int64_t t) {
-    int64_t c = t * n / total;
-    while ((c + 1) * total / n <= t) ++c;
-    while (c * total / n > t) --c;
-    return (int)c;
+  const int2 at = ws.at[x], before = ws.at[x - 1];
+  if (at.x < 0 || at.y == 0) return;                      // CTA x begins at a pair's first tile
+  if (before.x == at.x && before.y > 0) return;           // an earlier CTA begins inside the pair, too
+  const int pair = at.x, G = a.h_q / a.h_kv, rows = a.n * G;
+  // partial 0: CTA x - 1's last segment; partial i > 0: the first segment of CTA x - 1 + i
+  int parts = 2;
+  for (int y = x + 1; y < n_cta; y += 32) {
+    const int2 more = y + lane < n_cta ? ws.at[y + lane] : make_int2(-1, 0);
+    const unsigned in = __ballot_sync(kAll, more.x == pair && more.y > 0);
+    parts += in == kAll ? 32 : __ffs(~in) - 1;
+    if (in != kAll) break;
+  }
+  const int first = before.x == pair ? 0 : 1;
+  auto slot_of = [&](int i) {
+    return (int64_t)(2 * ((x - 1 + i) * row_groups + rg) + (i == 0 ? first : 0)) * slot_rows;
   };
-  const int c0 = holder(s0), c1 = holder(s1 - 1);
-  if (c0 == c1) return;  // written by the CTA itself
-  const int lr = blockIdx.y * kMergeWarps + warp, r = rg * group_rows + lr;
-  if (lr >= slot_rows || r >= a.n * G) return;
-  // partial i: CTA c0 + i; the first one is its CTA's last segment, the others' their first
-  const int parts = c1 - c0 + 1;
-  auto row_of = [&](int i) {
-    const int64_t c = c0 + i;
-    const int second = i == 0 && c * total / n < s0 ? 1 : 0;
-    return (2 * (c * row_groups + rg) + second) * (int64_t)slot_rows + lr;
-  };
-  float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, ws.ml[row_of(i)].x);
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-  float acc[D / 32], l = 0.f;
+  int lr[kMergeRows];
+  float M[kMergeRows], l[kMergeRows], acc[kMergeRows][D / 32];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+  for (int u = 0; u < kMergeRows; ++u) {
+    lr[u] = (blockIdx.y * kMergeWarps + warp) * kMergeRows + u;
+    if (lr[u] >= slot_rows) lr[u] = slot_rows - 1;  // (computed twice, written once)
+    M[u] = -INFINITY;
+    l[u] = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[u][e] = 0.f;
+  }
+  for (int i = lane; i < parts; i += 32)
+#pragma unroll
+    for (int u = 0; u < kMergeRows; ++u) M[u] = fmaxf(M[u], ws.ml[slot_of(i) + lr[u]].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < kMergeRows; ++u) M[u] = fmaxf(M[u], __shfl_xor_sync(kAll, M[u], o));
   for (int i0 = 0; i0 < parts; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < parts) {
-      const float2 ml = ws.ml[row_of(i0 + lane)];
-      w = merge_weight(ml.x, ml.y, M);
-      if (w != 0.f) l += w * ml.y;
+    float w[kMergeRows];
+#pragma unroll
+    for (int u = 0; u < kMergeRows; ++u) {
+      w[u] = 0.f;
+      if (i0 + lane < parts) {
+        const float2 ml = ws.ml[slot_of(i0 + lane) + lr[u]];
+        w[u] = merge_weight(ml.x, ml.y, M[u]);
+        if (w[u] != 0.f) l[u] += w[u] * ml.y;
+      }
     }
     const int m = min(32, parts - i0);
-#pragma unroll 4
+#pragma unroll 2
     for (int i = 0; i < m; ++i) {
-      const float wi = __shfl_sync(kAll, w, i);
-      const float4* o = reinterpret_cast<const float4*>(ws.o + row_of(i0 + i) * D);
 #pragma unroll
-      for (int q = 0; q < D / 128; ++q) {
-        const float4 x = o[q * 32 + lane];
-        if (wi != 0.f) {
-          acc[4 * q] += wi * x.x;
-          acc[4 * q + 1] += wi * x.y;
-          acc[4 * q + 2] += wi * x.z;
-          acc[4 * q + 3] += wi * x.w;
+      for (int u = 0; u < kMergeRows; ++u) {
+        const float wi = __shfl_sync(kAll, w[u], i);
+        const float4* o = reinterpret_cast<const float4*>(ws.o + (slot_of(i0 + i) + lr[u]) * D);
+#pragma unroll
+        for (int q = 0; q < D / 128; ++q) {
+          const float4 v = o[q * 32 + lane];
+          if (wi != 0.f) {
+            acc[u][4 * q] += wi * v.x;
+            acc[u][4 * q + 1] += wi * v.y;
+            acc[u][4 * q + 2] += wi * v.z;
+            acc[u][4 * q + 3] += wi * v.w;
+          }
         }
       }
     }
   }
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-  const float inv = inverse_sum(l);
   const int b = pair / a.h_kv, h = pair % a.h_kv;
-  uint16_t* out = a.out + (((int64_t)b * a.n + r / G) * a.h_q + (int64_t)h * G + r % G) * D;
 #pragma unroll
-  for (int q = 0; q < D / 128; ++q)
-    reinterpret_cast<uint2*>(out)[q * 32 + lane] =
-        make_uint2(pack_bf16x2(acc[4 * q] * inv, acc[4 * q + 1] * inv),
-                   pack_bf16x2(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
+  for (int u = 0; u < kMergeRows; ++u) {
+    float s = l[u];
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    const float inv = inverse_sum(s);
+    const int row = (blockIdx.y * kMergeWarps + warp) * kMergeRows + u, r = rg * group_rows + row;
+    if (row >= slot_rows || r >= rows) continue;
+    uint16_t* out = a.out + (((int64_t)b * a.n + r / G) * a.h_q + (int64_t)h * G + r % G) * D;
+#pragma unroll
+    for (int q = 0; q < D / 128; ++q)
+      reinterpret_cast<uint2*>(out)[q * 32 + lane] =
+          make_uint2(pack_bf16x2(acc[u][4 * q] * inv, acc[u][4 * q + 1] * inv),
+                     pack_bf16x2(acc[u][4 * q + 2] * inv, acc[u][4 * q + 3] * inv));
+  }
 }
 
 template <int D, bool TWO>
 cudaError_t launch_t(const TreeArgs& a, const Plan& plan, cudaStream_t s) {
+  using C = Cfg<D, TWO>;
   auto kern = tree_kernel<D, TWO>;
-  cudaError_t e = configure_kernel((const void*)kern, Cfg<D>::kSmem, false);
+  cudaError_t e = configure_kernel((const void*)kern, C::kSmem, false);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(plan.ctas, 1, 1);
-  cfg.blockDim = dim3(Cfg<D>::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, a, plan.row_groups, plan.slot_rows, tc_wait_limit());
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.batch * a.h_kv * plan.row_groups, (plan.slot_rows + kMergeWarps - 1) / kMergeWarps, 1);
+  if (plan.ctas == plan.row_groups) return cudaGetLastError();  // one CTA has every pair whole
+  cfg.gridDim = dim3(plan.ctas - plan.row_groups,
+                     (plan.slot_rows + kMergeWarps * kMergeRows - 1) / (kMergeWarps * kMergeRows), 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, plan.row_groups, plan.group_rows, plan.slot_rows,
@@ -829,7 +995,7 @@ size_t tree_ws_bytes(int batch, int n, int h_q, int h_kv, int d) {
   if (batch * h_kv == 0 || n == 0) return 0;
   const Plan p = plan_tree(n, h_q / h_kv, d);
   const size_t rows = 2 * (size_t)p.ctas * p.slot_rows;
-  return up256(((size_t)batch * h_kv + 3) * 8) + up256(rows * sizeof(float2)) + rows * d * sizeof(float);
+  return up256(p.ctas * sizeof(int2)) + up256(rows * sizeof(float2)) + rows * d * sizeof(float);
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
