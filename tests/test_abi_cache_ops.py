@@ -65,6 +65,7 @@ def _evict(lib, **kw):
     (dict(dst=None), NULL), (dict(lens=None), NULL), (dict(lo=None), NULL), (dict(k=None), NULL),
     (dict(lo=0x7000), SHAPE), (dict(dst=0x5000, dst_pages=4), SHAPE), (dict(dst_pages=0), SHAPE),
     (dict(sc=0x4008), ALIGN), (dict(mass=0x1002), ALIGN), (dict(v=0x3008), ALIGN),
+    (dict(batch=40000), UNSUPPORTED),
 ])
 def test_evict_refuses(lib, kw, status):
     assert _evict(lib, **kw) == status

@@ -575,6 +575,7 @@ int jssa_evict(const float* mass, int64_t mass_stride, jssa_bf16* k_cache, jssa_
                       score_bytes, block_table, max_pages, seq_lens, batch, h_kv, d, num_pages,
                       page_size, lens_out);
   if (st) return st;
+  if ((int64_t)batch * h_kv > 65535) return JSSA_ERR_UNSUPPORTED;  // one grid row per pair
   if ((st = check_paging(dst_max_pages, num_pages, page_size)) || batch == 0) return st;
   if (!dst_block_table || !idx || !count) return JSSA_ERR_NULL;
   if ((st = check_mass(mass, mass_stride, max_pages, page_size))) return st;

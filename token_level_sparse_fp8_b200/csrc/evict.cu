@@ -167,46 +167,78 @@ __global__ void __launch_bounds__(kCommitThreads)
 }
 
 // ---- evict ---------------------------------------------------------------------------------
-// A cluster of C CTAs per (sequence, KV head), C as large as fits one wave of one CTA per SM.
+// Selection: a cluster of C CTAs per (sequence, KV head), C as large as fits one wave.
 //   (1) The key of rank keep - recent among positions [0, L - recent): exact radix selection, 11 +
 //       11 + 10 bits, each CTA counting its slice of the positions; the C histograms are summed
 //       through distributed shared memory.
 //   (2) The kept positions in ascending order: each warp owns a contiguous range, counts its keys
 //       above and at the threshold, and writes its part after a scan over warps and CTAs.
-//   (3) The rows, in tiles of C x 128 (64 at d = 256). The rows of the next tile, the pages of the one after and the
-//       positions of the one after that are in flight while a tile is written.
-//   (4) Zeros in the mass of the positions left over.
-// Bound by HBM in (3) (a kept row is read once and written once) and by L2 latency in (1) and (2),
-// which pass five times over the 4 bytes of each position.
+// It passes five times over the 4 bytes of each position, the last four out of L2: bound by the
+// instructions of a pass. The rows then move (HBM-bound: each is read once and written once)
+//   * into other pages by a kernel of its own with a short-lived warp per few rows: nothing orders
+//     them, and many small blocks keep more rows in flight than a persistent loop (6.2 against 4.5
+//     TB/s of a copy of random 256-byte rows);
+//   * in place by the cluster that selected them, in tiles of C x 128 rows (64 at d = 256): the rows
+//     of the next tile, the pages of the one after and the positions of the one after that are in
+//     flight while a tile is written, with a cluster barrier between a tile's reads and its writes.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMaxCluster = 8;  // the portable size
 constexpr int kBins = 2048;          // four per thread
 constexpr int kFlight = 8;           // loads of mass in flight per lane
+constexpr int kClusterSpan = 8192;   // positions per CTA before more CTAs take part
 
 // Order-preserving key of a running mass; every NaN counts as the largest value.
+constexpr uint32_t kNanKey = 0xffffffffu;
 __device__ __forceinline__ uint32_t mass_key(float x) {
-  return x != x ? 0xffffffffu : score_key(x);
+  return x != x ? kNanKey : score_key(x);
+}
+// The value of a key other than NaN's (-0 has become +0, which compares the same).
+__device__ __forceinline__ float key_mass(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kEvictThreads, 1)
-    evict_kernel(RowMove m, EvictArgs e, int cluster, bool in_place) {
-  constexpr int kRows = D == 128 ? 8 : 4;  // per warp and tile: two tiles in registers
-  __shared__ __align__(16) uint32_t s_hist[2][kBins];  // alternating, so one barrier a round is enough
-  __shared__ __align__(16) uint4 s_counts;             // of this CTA: above, equal, first position out
-  __shared__ int s_above[kEvictWarps], s_equal[kEvictWarps], s_first, s_want;
-  __shared__ uint32_t s_bin, s_scan[kEvictWarps];
+// f(position, value, whether the position is in [lo, hi)) for a warp's positions, kFlight x 32 at a
+// time; every lane makes every call.
+template <class F>
+__device__ __forceinline__ void each_mass(const float* mass, int lo, int hi, int lane, F f) {
+  int p = lo;
+  for (; p + 32 * kFlight <= hi; p += 32 * kFlight) {
+    float x[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) x[u] = mass[p + 32 * u + lane];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) f(p + 32 * u + lane, x[u], true);
+  }
+#pragma unroll 1
+  for (; p < hi; p += 32) {
+    const int q = p + lane;
+    f(q, q < hi ? mass[q] : 0.f, q < hi);
+  }
+}
+
+struct SelectShared {
+  __align__(16) uint32_t hist[2][kBins];  // alternating, so one barrier a round is enough
+  __align__(16) uint4 counts;             // of this CTA: above, equal, first position out
+  int above[kEvictWarps], equal[kEvictWarps], first, want;
+  uint32_t bin, scan[kEvictWarps];
+};
+struct Kept {
+  int L, n_keep, first_out;  // length, positions kept, the first one that is not (or above)
+};
+
+// Writes idx, count and lens_out of the cluster's pair; on return they are visible to the cluster.
+__device__ __forceinline__ Kept select_kept(const RowMove& m, const EvictArgs& e, SelectShared& sh,
+                                            int cluster) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % cluster, pair = blockIdx.x / cluster;
   const int b = pair / m.h_kv, h = pair % m.h_kv;
   const int L = clamped_len(m, b, h == 0 && rank == 0 && tid == 0);
   const int n_keep = min(L, e.keep);
   const float* mass = e.mass + (int64_t)pair * e.mass_stride;
-  float* mass_out = e.mass_out + (int64_t)pair * e.mass_stride;
   int32_t* idx = e.idx + (int64_t)pair * e.keep;
   if (tid == 0) {
-    s_first = INT_MAX;
+    sh.first = INT_MAX;
     if (rank == 0) {
       e.count[pair] = n_keep;
       if (h == 0) m.lens_out[b] = n_keep;
@@ -216,42 +248,35 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
   // this warp's positions: the CTA's slice of [0, L), a 16th of it
   const int per_warp = ((L + cluster * kEvictWarps - 1) / (cluster * kEvictWarps) + 31) / 32 * 32;
   const int p_lo = min((int64_t)L, (int64_t)(rank * kEvictWarps + warp) * per_warp);
-  const int p_hi = min(L, p_lo + per_warp);
+  const int p_hi = max(p_lo, min(L, p_lo + per_warp));
   const int n_cand = L > e.keep ? L - e.recent : 0;  // positions that compete
   int want = L > e.keep ? e.keep - e.recent : 0;     // for so many places
   const bool pick = want > 0;
-  // (1)
   uint32_t edge = 0u;
   if (pick) {
 #pragma unroll 1
     for (int round = 0; round < 3; ++round) {
-      uint32_t* hist = s_hist[round & 1];
+      uint32_t* hist = sh.hist[round & 1];
       const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
       reinterpret_cast<uint4*>(hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       const int hi = min(p_hi, n_cand);
-      for (int p = p_lo; p < hi; p += 32 * kFlight) {
-        float x[kFlight];
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u)
-          if (p + 32 * u + lane < hi) x[u] = mass[p + 32 * u + lane];
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-          const bool in = p + 32 * u + lane < hi;
-          const uint32_t key = in ? mass_key(x[u]) : 0u;
-          const uint32_t bin = (key >> shift) & (kBins - 1);
-          if (round == 0) {
-            // (equal keys in a whole warp, as of untouched positions, would serialise)
-            const uint32_t bin0 = __shfl_sync(kAll, bin, 0);
-            if (__all_sync(kAll, in && bin == bin0)) {
-              if (lane == 0) atomicAdd(&hist[bin], 32u);
-            } else if (in) {
-              atomicAdd(&hist[bin], 1u);
-            }
-          } else if (in && (round == 1 ? key >> 21 == edge >> 21 : key >> 10 == edge >> 10)) {
-            atomicAdd(&hist[round == 1 ? bin : key & 1023u], 1u);
+      if (round == 0) {
+        each_mass(mass, p_lo, hi, lane, [&](int, float x, bool in) {
+          const uint32_t bin = mass_key(x) >> 21, bin0 = __shfl_sync(kAll, bin, 0);
+          // (equal keys in a whole warp, as of untouched positions, would serialise)
+          if (__all_sync(kAll, in && bin == bin0)) {
+            if (lane == 0) atomicAdd(&hist[bin], 32u);
+          } else if (in) {
+            atomicAdd(&hist[bin], 1u);
           }
-        }
+        });
+      } else {
+        const int low = round == 1 ? 21 : 10;  // bits below the prefix found so far
+        each_mass(mass, p_lo, hi, lane, [&](int, float x, bool in) {
+          const uint32_t key = mass_key(x);
+          if (in && (key ^ edge) >> low == 0u) atomicAdd(&hist[(key >> shift) & ((1u << (low - shift)) - 1u)], 1u);
+        });
       }
       if (cluster > 1) cluster_sync();
       else __syncthreads();
@@ -269,10 +294,10 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
         const uint32_t x = __shfl_up_sync(kAll, incl, o);
         if (lane >= o) incl += x;
       }
-      if (lane == 31) s_scan[warp] = incl;
+      if (lane == 31) sh.scan[warp] = incl;
       __syncthreads();
       uint32_t before = incl - mine;
-      for (int w = 0; w < warp; ++w) before += s_scan[w];
+      for (int w = 0; w < warp; ++w) before += sh.scan[w];
       if (before < (uint32_t)want && before + mine >= (uint32_t)want) {
         const uint32_t n[4] = {c.w, c.z, c.y, c.x};  // descending
         uint32_t left = want - before, bin = kBins - 1 - 4 * tid;
@@ -280,59 +305,55 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
           left -= n[u];
           --bin;
         }
-        s_want = left;
-        s_bin = bin;
+        sh.want = left;
+        sh.bin = bin;
       }
       __syncthreads();
-      want = s_want;  // keys to take of those with this prefix
-      edge |= s_bin << shift;
+      want = sh.want;  // keys to take of those with this prefix
+      edge |= sh.bin << shift;
     }
   }
   const int n_equal = pick ? want : 0;  // keys equal to the edge that stay, lowest positions first
-  // (2) 2: stays, 1: equal to the edge, 0: out; nothing is evicted when everything fits
-  auto state = [&](int p, float x) {
-    if (p >= L) return 0;
-    if (L <= e.keep || p >= n_cand) return 2;
-    if (!pick) return 0;
-    const uint32_t key = mass_key(x);
-    return key > edge ? 2 : key == edge ? 1 : 0;
-  };
+  // positions before n_cand stay if they are above the edge, or equal to it and early enough; those
+  // from n_cand on (the recent ones, or all when nothing is evicted) stay
+  const bool nan_edge = pick && edge == kNanKey;
+  const float edge_x = pick ? key_mass(edge) : 0.f;
+  auto is_above = [&](float x) { return pick && !nan_edge && !(x <= edge_x); };
+  auto is_equal = [&](float x) { return pick && (nan_edge ? x != x : x == edge_x); };
+  const int split = max(p_lo, min(p_hi, n_cand));  // this warp's first position that stays anyway
   int above = 0, equal = 0, first = INT_MAX;
-  for (int p = p_lo; p < p_hi; p += 32 * kFlight) {
-    float x[kFlight];
+  each_mass(mass, p_lo, split, lane, [&](int q, float x, bool in) {
+    const bool a = in && is_above(x);
+    above += a;
+    equal += in && is_equal(x);
+    if (in && !a) first = min(first, q);
+  });
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int q = p + 32 * u + lane;
-      x[u] = q < min(p_hi, n_cand) ? mass[q] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int q = p + 32 * u + lane, s = q < p_hi ? state(q, x[u]) : -1;
-      above += __popc(__ballot_sync(kAll, s == 2));
-      equal += __popc(__ballot_sync(kAll, s == 1));
-      const unsigned out = __ballot_sync(kAll, s == 0 || s == 1);
-      if (out && first == INT_MAX) first = p + 32 * u + __ffs(out) - 1;
-    }
+  for (int o = 16; o; o >>= 1) {
+    above += __shfl_xor_sync(kAll, above, o);
+    equal += __shfl_xor_sync(kAll, equal, o);
+    first = min(first, __shfl_xor_sync(kAll, first, o));
   }
+  above += p_hi - split;
   if (lane == 0) {
-    s_above[warp] = above;
-    s_equal[warp] = equal;
-    if (first != INT_MAX) atomicMin(&s_first, first);
+    sh.above[warp] = above;
+    sh.equal[warp] = equal;
+    if (first != INT_MAX) atomicMin(&sh.first, first);
   }
   __syncthreads();
   if (warp == 0) {
-    int a = lane < kEvictWarps ? s_above[lane] : 0, q = lane < kEvictWarps ? s_equal[lane] : 0;
+    int a = lane < kEvictWarps ? sh.above[lane] : 0, q = lane < kEvictWarps ? sh.equal[lane] : 0;
     for (int o = 16; o; o >>= 1) {
       a += __shfl_xor_sync(kAll, a, o);
       q += __shfl_xor_sync(kAll, q, o);
     }
-    if (lane == 0) s_counts = make_uint4(a, q, s_first, 0u);
+    if (lane == 0) sh.counts = make_uint4(a, q, sh.first, 0u);
   }
   if (cluster > 1) cluster_sync();
   else __syncthreads();
   int base = 0, eq_before = 0, first_out = INT_MAX;
   for (int r = 0; r < cluster; ++r) {
-    const uint32_t at = smem_u32(&s_counts);
+    const uint32_t at = smem_u32(&sh.counts);
     const uint4 c = cluster > 1 ? ld_cluster_v4(cluster_addr(at, r)) : ld_shared_v4(at);
     first_out = min(first_out, (int)c.z);
     if (r < rank) {
@@ -341,84 +362,159 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
     }
   }
   for (int w = 0; w < warp; ++w) {
-    base += s_above[w] + max(0, min(s_equal[w], n_equal - eq_before));
-    eq_before += s_equal[w];
+    base += sh.above[w] + max(0, min(sh.equal[w], n_equal - eq_before));
+    eq_before += sh.equal[w];
   }
   const unsigned below = (1u << lane) - 1u;
-  for (int p = p_lo; p < p_hi; p += 32 * kFlight) {
-    float x[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int q = p + 32 * u + lane;
-      x[u] = q < min(p_hi, n_cand) ? mass[q] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int q = p + 32 * u + lane, s = q < p_hi ? state(q, x[u]) : -1;
-      const unsigned eq = __ballot_sync(kAll, s == 1);
-      const bool stay = s == 2 || (s == 1 && eq_before + __popc(eq & below) < n_equal);
-      const unsigned st = __ballot_sync(kAll, stay);
-      if (stay) __stcg(&idx[base + __popc(st & below)], q);
-      base += __popc(st);
+  each_mass(mass, p_lo, split, lane, [&](int q, float x, bool in) {
+    const unsigned eq = __ballot_sync(kAll, in && is_equal(x));
+    bool stay = in && is_above(x);
+    if (eq) {
+      stay = stay || (in && is_equal(x) && eq_before + __popc(eq & below) < n_equal);
       eq_before += __popc(eq);
     }
-  }
+    const unsigned st = __ballot_sync(kAll, stay);
+    if (stay) __stcg(&idx[base + __popc(st & below)], q);
+    base += __popc(st);
+  });
+  for (int q = split + lane; q < p_hi; q += 32) __stcg(&idx[base + q - split], q);
   for (int i = n_keep + rank * kEvictThreads + tid; i < e.keep; i += cluster * kEvictThreads) idx[i] = -1;
   if (cluster > 1) cluster_sync();
   else __syncthreads();
-  // (3) in place, the rows before the first one out stay where they are
+  return {L, n_keep, first_out};
+}
+
+// Selection alone, and zeros in the mass of the positions left over (mass_out is not mass).
+__global__ void __launch_bounds__(kEvictThreads, 2) select_kernel(RowMove m, EvictArgs e, int cluster) {
+  __shared__ SelectShared sh;
+  const Kept k = select_kept(m, e, sh, cluster);
+  const int rank = blockIdx.x % cluster, pair = blockIdx.x / cluster;
+  float* mass_out = e.mass_out + (int64_t)pair * e.mass_stride;
+  for (int p = k.n_keep + rank * kEvictThreads + threadIdx.x; p < k.L; p += cluster * kEvictThreads)
+    mass_out[p] = 0.f;
+}
+
+// Looks up a row's pages; they may still be in flight on return (see usable).
+__device__ __forceinline__ Ends look_up(const RowMove& m, const EvictArgs& e, const int32_t* table,
+                                        const int32_t* dst_table, int src, int dst) {
+  Ends r = {-1, -1, -1, -1};
+  if (src >= 0) {
+    r.src_pos = src;
+    r.dst_pos = dst;
+    r.src_pg = src < m.max_pages * m.page_size ? table[src / m.page_size] : -2;
+    r.dst_pg = dst < e.dst_max_pages * m.page_size ? dst_table[dst / m.page_size] : -2;
+  }
+  return r;
+}
+// Both pages have to be usable (-2: beyond the table).
+__device__ __forceinline__ void usable(const RowMove& m, Ends& r) {
+  if (r.src_pos < 0) return;
+  const bool beyond = r.src_pg == -2 || r.dst_pg == -2;
+  const bool bad = (r.src_pg != -2 && (r.src_pg < 0 || r.src_pg >= m.num_pages)) ||
+                   (r.dst_pg != -2 && (r.dst_pg < 0 || r.dst_pg >= m.num_pages));
+  if (beyond || bad) {
+    raise_flag((beyond ? 2u : 0u) | (bad ? 1u : 0u));
+    r.src_pg = r.dst_pg = -1;
+  }
+}
+
+// The rows of one eviction into other pages: grid (row blocks, pairs), 32 rows per warp. Lane u looks
+// up row u; the K / V chunks then go through registers in groups, one being read while one is written.
+constexpr int kMoveThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(RowMove m, EvictArgs e) {
+  constexpr int kGroup = D == 128 ? 4 : 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pair = blockIdx.y, b = pair / m.h_kv, h = pair % m.h_kv;
+  pdl_wait();
+  const int i = (blockIdx.x * (kMoveThreads / 32) + warp) * 32 + lane;
+  const int src = i < e.keep ? e.idx[(int64_t)pair * e.keep + i] : -1;  // (-1: padding)
+  if (__all_sync(kAll, src < 0)) return;
+  Ends ends = look_up(m, e, m.block_table + (int64_t)b * m.max_pages,
+                      e.dst_table + (int64_t)b * e.dst_max_pages, src, i);
+  usable(m, ends);
+  const int64_t from = ends.src_pg >= 0 ? kv_offset(m, ends.src_pg, ends.src_pos, h) : -1;
+  const int64_t to = ends.dst_pg >= 0 ? kv_offset(m, ends.dst_pg, ends.dst_pos, h) : -1;
+  LaneRow<D> x[2][kGroup];
+  auto read = [&](LaneRow<D>(&r)[kGroup], int g) {
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) {
+      const int64_t off = __shfl_sync(kAll, from, g * kGroup + u);
+      if (off >= 0) r[u].load(m.k_cache, m.v_cache, off, lane);
+    }
+  };
+  auto write = [&](const LaneRow<D>(&r)[kGroup], int g) {
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) {
+      const int64_t off = __shfl_sync(kAll, to, g * kGroup + u);
+      if (off >= 0) r[u].store(m.k_cache, m.v_cache, off, lane);
+    }
+  };
+  read(x[0], 0);
+  // mass: lane u's row; scoring codes: 16-byte chunks, `per` of a row side by side
+  const float mass = src >= 0 ? e.mass[(int64_t)pair * e.mass_stride + src] : 0.f;
+  if (src >= 0) e.mass_out[(int64_t)pair * e.mass_stride + i] = mass;
+#pragma unroll 1
+  for (int g = 0; g < 32 / kGroup; g += 2) {
+    read(x[1], g + 1);
+    write(x[0], g);
+    if (g + 2 < 32 / kGroup) read(x[0], g + 2);
+    write(x[1], g + 1);
+  }
+  const int per = m.code_bytes >> 4;
+#pragma unroll 1
+  for (int c = 0; c < per; ++c) {
+    const int u = (c * 32 + lane) / per, at = (c * 32 + lane) % per * 16;
+    const int sp = __shfl_sync(kAll, ends.src_pg, u), ss = __shfl_sync(kAll, ends.src_pos, u);
+    const int dp = __shfl_sync(kAll, ends.dst_pg, u), ds = __shfl_sync(kAll, ends.dst_pos, u);
+    if (sp >= 0)
+      *reinterpret_cast<uint4*>(m.score_cache + code_offset(m, dp, ds, h) + at) =
+          *reinterpret_cast<const uint4*>(m.score_cache + code_offset(m, sp, ss, h) + at);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kEvictThreads, 1)
+    evict_in_place_kernel(RowMove m, EvictArgs e, int cluster) {
+  constexpr int kRows = D == 128 ? 8 : 4;  // per warp and tile: two tiles in registers
+  __shared__ SelectShared sh;
+  const Kept k = select_kept(m, e, sh, cluster);
+  const int L = k.L, n_keep = k.n_keep;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % cluster, pair = blockIdx.x / cluster;
+  const int b = pair / m.h_kv, h = pair % m.h_kv;
+  const float* mass = e.mass + (int64_t)pair * e.mass_stride;
+  float* mass_out = e.mass_out + (int64_t)pair * e.mass_stride;
+  const int32_t* idx = e.idx + (int64_t)pair * e.keep;
+  // the rows before the first one out stay where they are (unless the mass or the pages are others)
   const int32_t* table = m.block_table + (int64_t)b * m.max_pages;
   const int32_t* dst_table = e.dst_table + (int64_t)b * e.dst_max_pages;
   const int span = cluster * kEvictWarps * kRows;
   const bool stays = e.dst_table == m.block_table && e.mass_out == e.mass;
-  const int i_begin = stays ? min(first_out, n_keep) : 0;
+  const int i_begin = stays ? min(k.first_out, n_keep) : 0;
   const int n_tiles = (n_keep - i_begin + span - 1) / span;
   const int row0 = i_begin + (rank * kEvictWarps + warp) * kRows + lane;  // (the first lanes)
   auto position = [&](int t) {  // of this lane's row of tile t; -1: none
     const int i = row0 + t * span;
     return lane < kRows && t < n_tiles && i < n_keep ? __ldcg(&idx[i]) : -1;
   };
-  const int src_len = m.max_pages * m.page_size, dst_len = e.dst_max_pages * m.page_size;
-  auto look_up = [&](int t, int pos) {
-    Ends r = {-1, -1, -1, -1};
-    if (pos >= 0) {
-      const int i = row0 + t * span;
-      r.src_pos = pos;
-      r.dst_pos = i;
-      r.src_pg = pos < src_len ? table[pos / m.page_size] : -2;
-      r.dst_pg = i < dst_len ? dst_table[i / m.page_size] : -2;
-    }
-    return r;
-  };
-  auto check = [&](Ends& r) {  // both pages have to be usable (-2: beyond the table)
-    if (r.src_pos < 0) return;
-    const uint32_t bad = (r.src_pg == -2 || r.dst_pg == -2 ? 2u : 0u) |
-                         ((r.src_pg != -2 && (r.src_pg < 0 || r.src_pg >= m.num_pages)) ||
-                                  (r.dst_pg != -2 && (r.dst_pg < 0 || r.dst_pg >= m.num_pages))
-                              ? 1u : 0u);
-    if (bad) {
-      raise_flag(bad);
-      r.src_pg = r.dst_pg = -1;
-    }
-  };
+  auto ends_of = [&](int t, int pos) { return look_up(m, e, table, dst_table, pos, row0 + t * span); };
   // a step writes tile t (`cur`) after the reads of tile t + 1 (`nxt`) have been issued
   WarpTile<D, kRows> ta, tb;
   Ends ea, eb, ahead;
-  ea = look_up(0, position(0));
-  ahead = look_up(1, position(1));
+  ea = ends_of(0, position(0));
+  ahead = ends_of(1, position(1));
   int pos = position(2);
-  check(ea);
+  usable(m, ea);
   ta.load(m, h, mass, ea, lane);
   auto step = [&](int t, const WarpTile<D, kRows>& cur, const Ends& ce, WarpTile<D, kRows>& nxt, Ends& ne) {
     ne = ahead;
-    check(ne);
+    usable(m, ne);
     nxt.load(m, h, mass, ne, lane);
-    ahead = look_up(t + 2, pos);
+    ahead = ends_of(t + 2, pos);
     pos = position(t + 3);
-    if (in_place) {
-      if (cluster > 1) cluster_sync();
-      else __syncthreads();
-    }
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
     cur.store(m, h, mass_out, ce, lane);
   };
 #pragma unroll 1
@@ -426,7 +522,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
     step(t, ta, ea, tb, eb);
     if (t + 1 < n_tiles) step(t + 1, tb, eb, ta, ea);
   }
-  // (4) (in place, the last tile's barrier came after the last read of the mass)
+  // (the last tile's barrier came after the last read of the mass)
   for (int p = n_keep + rank * kEvictThreads + tid; p < L; p += cluster * kEvictThreads) mass_out[p] = 0.f;
 }
 
@@ -447,9 +543,13 @@ cudaError_t launch_evict(const RowMove& m, const EvictArgs& e, cudaStream_t s) {
   using namespace evict_detail;
   const int pairs = m.batch * m.h_kv;
   if (pairs == 0) return cudaSuccess;
-  int cluster = 1;
-  while (cluster < kEvictMaxCluster && 2 * cluster * pairs <= num_sms()) cluster *= 2;
   const bool in_place = e.dst_table == m.block_table || e.mass_out == e.mass;
+  const int slots = (in_place ? 1 : 2) * num_sms();  // CTAs of one wave
+  // a round over a cluster costs some 3 us more than one inside a CTA (barriers, remote reads), about
+  // what a CTA takes for kClusterSpan more positions; in place the cluster also shares the moves
+  const int64_t len = (int64_t)m.max_pages * m.page_size, span = in_place ? kClusterSpan / 4 : kClusterSpan;
+  int cluster = 1;
+  while (cluster < kEvictMaxCluster && 2 * cluster * pairs <= slots && cluster * span < len) cluster *= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
@@ -460,9 +560,20 @@ cudaError_t launch_evict(const RowMove& m, const EvictArgs& e, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t err = cudaErrorInvalidValue;
-  if (m.d == 128) err = cudaLaunchKernelEx(&cfg, evict_kernel<128>, m, e, cluster, in_place);
-  else if (m.d == 256) err = cudaLaunchKernelEx(&cfg, evict_kernel<256>, m, e, cluster, in_place);
+  if (in_place) {
+    const cudaError_t err = m.d == 128 ? cudaLaunchKernelEx(&cfg, evict_in_place_kernel<128>, m, e, cluster)
+                                       : cudaLaunchKernelEx(&cfg, evict_in_place_kernel<256>, m, e, cluster);
+    return err != cudaSuccess ? err : cudaGetLastError();
+  }
+  cudaError_t err = cudaLaunchKernelEx(&cfg, select_kernel, m, e, cluster);
+  if (err != cudaSuccess) return err;
+  const int rows = kMoveThreads;
+  cfg.gridDim = dim3((e.keep + rows - 1) / rows, pairs, 1);
+  cfg.blockDim = dim3(kMoveThreads, 1, 1);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  err = m.d == 128 ? cudaLaunchKernelEx(&cfg, move_kernel<128>, m, e)
+                   : cudaLaunchKernelEx(&cfg, move_kernel<256>, m, e);
   if (err != cudaSuccess) return err;
   return cudaGetLastError();
 }
