@@ -117,63 +117,89 @@ def _ws_bytes(fn, batch, h_q, h_kv, d, max_pages, page_size, budget, device_inde
     return workspace_size(fn, batch, h_q, h_kv, d, max_pages, page_size, budget)
 
 
-def _call_on(device: torch.device, name: str, *args) -> None:
-    """Call an entry point with ``device`` current, on its current stream."""
-    if torch.cuda.current_device() == device.index:
-        call(name, *args, _stream(device))
+_entries = {}
+
+
+def _call_on(index: int, name: str, *args) -> None:
+    """Call an entry point with device ``index`` current, on its current stream."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(load(), name)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            call(name, *args, _stream(device))
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(name, status)
 
 
 def _shape(t: torch.Tensor, name: str, shape, device: torch.device):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _need_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, h_kv=None, d=None):
-    """(strides, num_pages, page_size, h_kv, d) of a K / V cache pair."""
+def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, shape, like: torch.Tensor) -> int:
+    """Pointer of a contiguous tensor of that type and shape on the device of ``like``."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device()
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype)
+    _shape(t, name, shape, like.device)
+    return t.data_ptr()
+
+
+def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor):
+    """(pointers, strides, shape) of a K / V cache pair ``[num_pages, page_size, h_kv, d]``."""
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
-    strides = kv_strides(k_cache)
-    if kv_strides(v_cache) != strides or v_cache.shape != k_cache.shape:
+    strides, shape = k_cache.stride(), k_cache.shape
+    if len(shape) != 4 or strides[3] != 1:
+        raise ValueError("KV cache must be [num_pages, page_size, h_kv, d] with a contiguous last dim")
+    if v_cache.stride() != strides or v_cache.shape != shape:
         raise ValueError("K and V caches must share one layout")
-    if v_cache.device != k_cache.device:
+    if v_cache.get_device() != k_cache.get_device():
         raise ValueError("K and V caches must be on one device")
-    return (strides, *k_cache.shape)
+    return (k_cache.data_ptr(), v_cache.data_ptr()), strides[:3], shape
 
 
-def _need_table(block_table, seq_lens, device, batch=None, name="block_table"):
-    _need(block_table, name, torch.int32)
-    if block_table.dim() != 2 or (batch is not None and block_table.shape[0] != batch):
-        raise ValueError(f"{name} must be [batch, max_pages]")
-    if block_table.device != device:
-        raise ValueError(f"{name} must be on {device}, got {block_table.device}")
-    if seq_lens is not None:
-        _need(seq_lens, "seq_lens", torch.int32)
-        _shape(seq_lens, "seq_lens", (block_table.shape[0],), device)
+def _table(t: torch.Tensor, name: str, batch: int, like: torch.Tensor):
+    """(pointer, width) of an int32 page table of ``batch`` rows."""
+    width = t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() == 2 else 0
+    return _arg(t, name, torch.int32, (batch, width), like), width
 
 
-def _need_mass(mass, name, batch, h_kv, capacity, device):
-    _need(mass, name, torch.float32)
-    if mass.dim() != 3 or mass.shape[:2] != (batch, h_kv) or mass.shape[2] < capacity:
+def _mass(t: torch.Tensor, name: str, batch: int, h_kv: int, capacity: int, like: torch.Tensor):
+    """(pointer, row length) of running masses ``[batch, h_kv, >= capacity]``."""
+    row = t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() == 3 else 0
+    p = _arg(t, name, torch.float32, (batch, h_kv, row), like)
+    if row < capacity:
         raise ValueError(f"{name} must be [batch, h_kv, >= max_pages * page_size]")
-    if mass.device != device:
-        raise ValueError(f"{name} must be on {device}, got {mass.device}")
+    return p, row
 
 
-def _need_codes(score_cache, num_pages, h_kv, page_size, device):
-    """Bytes of a scoring row (0 without a scoring cache)."""
+def _codes(score_cache: Optional[torch.Tensor], num_pages, h_kv, page_size, like: torch.Tensor):
+    """(pointer, bytes of a scoring row) of a scoring cache; (None, 0) without one."""
     if score_cache is None:
-        return 0
-    bf16 = score_cache.dtype == torch.bfloat16
-    _need(score_cache, "score_cache", torch.bfloat16 if bf16 else torch.uint8)
-    if score_cache.dim() != 4:
-        raise ValueError("score_cache must be [num_pages, h_kv, page_size, r]")
-    _shape(score_cache, "score_cache", (num_pages, h_kv, page_size, score_cache.shape[3]), device)
-    return score_cache.shape[3] * (2 if bf16 else 1)
+        return None, 0
+    bf16 = isinstance(score_cache, torch.Tensor) and score_cache.dtype is torch.bfloat16
+    r = score_cache.shape[-1] if isinstance(score_cache, torch.Tensor) and score_cache.dim() == 4 else 0
+    p = _arg(score_cache, "score_cache", torch.bfloat16 if bf16 else torch.uint8,
+             (num_pages, h_kv, page_size, r), like)
+    return p, r * (2 if bf16 else 1)
+
+
+def _or_new(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> torch.Tensor:
+    """An int32 output: the caller's, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=like.device)
+    _arg(t, name, torch.int32, shape, like)
+    return t
 
 
 # ------------------------------------------------------------------------------------------------
@@ -431,17 +457,16 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     out = torch.empty_like(q) if out is None else out
     if mass is not None:
-        _need_table(block_table, None, q.device, batch)
-        _shape(idx, "idx", (batch, h_kv, budget), q.device)
-        _shape(count, "count", (batch, h_kv), q.device)
-        _need_mass(mass, "mass", batch, h_kv, block_table.shape[1] * page_size, q.device)
-        p, n, _hold = _scratch(ws, _ws_bytes(FN_INDEXED_ATTEND_MASS, batch, h_q, h_kv, d,
-                                             block_table.shape[1], page_size, budget,
-                                             q.device.index), q.device)
-        _call_on(q.device, "jssa_indexed_attend_mass", q.data_ptr(), k_cache.data_ptr(),
-                 v_cache.data_ptr(), *strides, block_table.data_ptr(), block_table.shape[1],
-                 idx.data_ptr(), count.data_ptr(), batch, h_q, h_kv, d, budget, num_pages,
-                 page_size, scale, mass.data_ptr(), mass.shape[2], out.data_ptr(), p, n)
+        bt, max_pages = _table(block_table, "block_table", batch, q)
+        m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
+        i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
+        c = _arg(count, "count", torch.int32, (batch, h_kv), q)
+        o = _arg(out, "out", torch.bfloat16, q.shape, q)
+        p, n, _hold = _scratch(ws, _ws_bytes(FN_INDEXED_ATTEND_MASS, batch, h_q, h_kv, d, max_pages,
+                                             page_size, budget, q.get_device()), q.device)
+        _call_on(q.get_device(), "jssa_indexed_attend_mass", q.data_ptr(), k_cache.data_ptr(),
+                 v_cache.data_ptr(), *strides, bt, max_pages, i, c, batch, h_q, h_kv, d, budget,
+                 num_pages, page_size, scale, m, row, o, p, n)
         return out
     w = _ws(q.device, ws, FN_INDEXED_ATTEND)
     p, n = w.get(workspace_size(FN_INDEXED_ATTEND, batch, h_q, h_kv, d, block_table.shape[1],
@@ -587,14 +612,15 @@ def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     out = torch.empty_like(q) if out is None else out
     if mass is not None:
-        _need_table(block_table, seq_lens, q.device, batch)
-        _need_mass(mass, "mass", batch, h_kv, max_pages * page_size, q.device)
+        bt, max_pages = _table(block_table, "block_table", batch, q)
+        m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
+        lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
+        o = _arg(out, "out", torch.bfloat16, q.shape, q)
         p, n, _hold = _scratch(ws, _ws_bytes(FN_DENSE_DECODE_MASS, batch, h_q, h_kv, d, max_pages,
-                                             page_size, window, q.device.index), q.device)
-        _call_on(q.device, "jssa_dense_decode_mass", q.data_ptr(), k_cache.data_ptr(),
-                 v_cache.data_ptr(), *strides, block_table.data_ptr(), max_pages,
-                 seq_lens.data_ptr(), batch, h_q, h_kv, d, num_pages, page_size, window, scale,
-                 mass.data_ptr(), mass.shape[2], out.data_ptr(), p, n)
+                                             page_size, window, q.get_device()), q.device)
+        _call_on(q.get_device(), "jssa_dense_decode_mass", q.data_ptr(), k_cache.data_ptr(),
+                 v_cache.data_ptr(), *strides, bt, max_pages, lens, batch, h_q, h_kv, d, num_pages,
+                 page_size, window, scale, m, row, o, p, n)
         return out
     w = _ws(q.device, ws, FN_DENSE_DECODE)
     p, n = w.get(workspace_size(FN_DENSE_DECODE, batch, h_q, h_kv, d, max_pages, page_size, window))
@@ -636,19 +662,18 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
     if count is None:
         count = torch.empty((batch, h_kv), dtype=torch.int32, device=q.device)
     if mass is not None:
-        _need_table(block_table, seq_lens, q.device, batch)
-        _shape(idx, "idx", (batch, h_kv, budget), q.device)
-        _shape(count, "count", (batch, h_kv), q.device)
-        _need_mass(mass, "mass", batch, h_kv, block_table.shape[1] * page_size, q.device)
-        p, n, _hold = _scratch(ws, _ws_bytes(FN_DECODE_MASS, batch, h_q, h_kv, d,
-                                             block_table.shape[1], page_size, budget,
-                                             q.device.index), q.device)
-        _call_on(q.device, "jssa_decode_mass", q.data_ptr(), _ptr(k_new), _ptr(v_new),
+        bt, max_pages = _table(block_table, "block_table", batch, q)
+        m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
+        lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
+        i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
+        c = _arg(count, "count", torch.int32, (batch, h_kv), q)
+        o = _arg(out, "out", torch.bfloat16, q.shape, q)
+        p, n, _hold = _scratch(ws, _ws_bytes(FN_DECODE_MASS, batch, h_q, h_kv, d, max_pages,
+                                             page_size, budget, q.get_device()), q.device)
+        _call_on(q.get_device(), "jssa_decode_mass", q.data_ptr(), _ptr(k_new), _ptr(v_new),
                  k_cache.data_ptr(), v_cache.data_ptr(), *strides, score_cache.data_ptr(),
-                 basis.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                 seq_lens.data_ptr(), batch, h_q, h_kv, d, r, num_pages, page_size, budget, scale,
-                 mass.data_ptr(), mass.shape[2], idx.data_ptr(), count.data_ptr(), out.data_ptr(),
-                 p, n)
+                 basis.data_ptr(), bt, max_pages, lens, batch, h_q, h_kv, d, r, num_pages,
+                 page_size, budget, scale, m, row, i, c, o, p, n)
         return out, idx, count
     w = _ws(q.device, ws, FN_DECODE)
     p, n = w.get(workspace_size(FN_DECODE, batch, h_q, h_kv, d, block_table.shape[1], page_size,
@@ -686,41 +711,38 @@ def tree_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if q.dim() != 4:
         raise ValueError("q must be [batch, n, h_q, d]")
     batch, n, h_q, d = q.shape
-    dev = q.device
-    strides, num_pages, page_size, h_kv, dc = _need_cache(k_cache, v_cache)
-    if dc != d or k_cache.device != dev:
+    kv, strides, (num_pages, page_size, h_kv, dc) = _caches(k_cache, v_cache)
+    index = q.get_device()
+    if dc != d or k_cache.get_device() != index:
         raise ValueError("q and the caches must agree on the head dim and the device")
-    _need_table(block_table, seq_lens, dev, batch)
-    _need(parents, "parents", torch.int32)
-    _shape(parents, "parents", (batch, n), dev)
+    bt, max_pages = _table(block_table, "block_table", batch, q)
+    lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
+    par = _arg(parents, "parents", torch.int32, (batch, n), q)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
+    kn = vn = None
     if k_new is not None:
-        _need(k_new, "k_new", torch.bfloat16)
-        _need(v_new, "v_new", torch.bfloat16)
-        _shape(k_new, "k_new", (batch, n, h_kv, d), dev)
-        _shape(v_new, "v_new", (batch, n, h_kv, d), dev)
+        kn = _arg(k_new, "k_new", torch.bfloat16, (batch, n, h_kv, d), q)
+        vn = _arg(v_new, "v_new", torch.bfloat16, (batch, n, h_kv, d), q)
     if (idx is None) != (count is None):
         raise ValueError("idx and count go together")
+    i = c = None
     budget = 0
     if idx is not None:
-        _need(idx, "idx", torch.int32)
-        _need(count, "count", torch.int32)
         budget = idx.shape[-1]
-        _shape(idx, "idx", (batch, h_kv, budget), dev)
-        _shape(count, "count", (batch, h_kv), dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
+        i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
+        c = _arg(count, "count", torch.int32, (batch, h_kv), q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need(out, "out", torch.bfloat16)
-        _shape(out, "out", (batch, n, h_q, d), dev)
-    p, nb, _hold = _scratch(ws, _ws_bytes(FN_TREE_ATTEND, batch, h_q, h_kv, d,
-                                          block_table.shape[1], page_size, n, dev.index), dev)
-    _call_on(dev, "jssa_tree_attend", q.data_ptr(), _ptr(k_new), _ptr(v_new), k_cache.data_ptr(),
-             v_cache.data_ptr(), *strides, block_table.data_ptr(), block_table.shape[1],
-             seq_lens.data_ptr(), parents.data_ptr(), _ptr(idx), _ptr(count), batch, n, h_q, h_kv,
-             d, budget, num_pages, page_size, window, scale, out.data_ptr(), p, nb)
+        _arg(out, "out", torch.bfloat16, q.shape, q)
+    p, nb, _hold = _scratch(ws, _ws_bytes(FN_TREE_ATTEND, batch, h_q, h_kv, d, max_pages, page_size,
+                                          n, index), q.device)
+    _call_on(index, "jssa_tree_attend", q.data_ptr(), kn, vn, *kv, *strides, bt, max_pages, lens,
+             par, i, c, batch, n, h_q, h_kv, d, budget, num_pages, page_size, window, scale,
+             out.data_ptr(), p, nb)
     return out
 
 
@@ -732,24 +754,17 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
     code) of position ``seq_lens[b] + path[b, i]`` moves to ``seq_lens[b] + i``. ``path`` int32
     ``[batch, <= 64]`` (node indices), ``n_path`` int32 ``[batch]``. Returns the new lengths
     (int32 ``[batch]``; ``seq_lens`` itself is left as it is)."""
-    strides, num_pages, page_size, h_kv, d = _need_cache(k_cache, v_cache)
-    dev = k_cache.device
-    _need_table(block_table, seq_lens, dev)
+    kv, strides, (num_pages, page_size, h_kv, d) = _caches(k_cache, v_cache)
     batch = block_table.shape[0]
-    _need(path, "path", torch.int32)
-    _need(n_path, "n_path", torch.int32)
-    _shape(path, "path", (batch, path.shape[-1]), dev)
-    _shape(n_path, "n_path", (batch,), dev)
-    code = _need_codes(score_cache, num_pages, h_kv, page_size, dev)
-    if lens is None:
-        lens = torch.empty_like(seq_lens)
-    else:
-        _need(lens, "lens", torch.int32)
-        _shape(lens, "lens", (batch,), dev)
-    _call_on(dev, "jssa_tree_commit", k_cache.data_ptr(), v_cache.data_ptr(), *strides,
-             _ptr(score_cache), code, block_table.data_ptr(), block_table.shape[1],
-             seq_lens.data_ptr(), path.data_ptr(), n_path.data_ptr(), path.shape[1], batch, h_kv, d,
-             num_pages, page_size, lens.data_ptr())
+    bt, max_pages = _table(block_table, "block_table", batch, k_cache)
+    sl = _arg(seq_lens, "seq_lens", torch.int32, (batch,), k_cache)
+    max_path = path.shape[-1]
+    pa = _arg(path, "path", torch.int32, (batch, max_path), k_cache)
+    n_pa = _arg(n_path, "n_path", torch.int32, (batch,), k_cache)
+    sc, code = _codes(score_cache, num_pages, h_kv, page_size, k_cache)
+    lens = _or_new(lens, "lens", (batch,), k_cache)
+    _call_on(k_cache.get_device(), "jssa_tree_commit", *kv, *strides, sc, code, bt, max_pages, sl,
+             pa, n_pa, max_path, batch, h_kv, d, num_pages, page_size, lens.data_ptr())
     return lens
 
 
@@ -767,42 +782,26 @@ def evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     None), whose entries from there to the old length become zero. Returns
     ``(idx, count, lens)``: the kept positions int32 ``[batch, h_kv, keep]`` (ascending, -1
     padded), their number, and the new lengths int32 ``[batch]`` (``seq_lens`` is left as it is)."""
-    strides, num_pages, page_size, h_kv, d = _need_cache(k_cache, v_cache)
-    dev = k_cache.device
-    _need_table(block_table, seq_lens, dev)
-    batch, max_pages = block_table.shape
-    _need_mass(mass, "mass", batch, h_kv, max_pages * page_size, dev)
-    if mass_out is None:
-        mass_out = mass
-    else:
-        _need_mass(mass_out, "mass_out", batch, h_kv, max_pages * page_size, dev)
-        if mass_out.shape[2] != mass.shape[2]:
+    kv, strides, (num_pages, page_size, h_kv, d) = _caches(k_cache, v_cache)
+    batch = block_table.shape[0]
+    bt, max_pages = _table(block_table, "block_table", batch, k_cache)
+    sl = _arg(seq_lens, "seq_lens", torch.int32, (batch,), k_cache)
+    m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, k_cache)
+    mo = m
+    if mass_out is not None:
+        mo, row_out = _mass(mass_out, "mass_out", batch, h_kv, max_pages * page_size, k_cache)
+        if row_out != row:
             raise ValueError("mass and mass_out must have the same shape")
-    code = _need_codes(score_cache, num_pages, h_kv, page_size, dev)
-    if dst_block_table is None:
-        dst_block_table = block_table
-    else:
-        _need_table(dst_block_table, None, dev, batch, "dst_block_table")
-    if idx is None:
-        idx = torch.empty((batch, h_kv, keep), dtype=torch.int32, device=dev)
-    else:
-        _need(idx, "idx", torch.int32)
-        _shape(idx, "idx", (batch, h_kv, keep), dev)
-    if count is None:
-        count = torch.empty((batch, h_kv), dtype=torch.int32, device=dev)
-    else:
-        _need(count, "count", torch.int32)
-        _shape(count, "count", (batch, h_kv), dev)
-    if lens is None:
-        lens = torch.empty_like(seq_lens)
-    else:
-        _need(lens, "lens", torch.int32)
-        _shape(lens, "lens", (batch,), dev)
-    _call_on(dev, "jssa_evict", mass.data_ptr(), mass.shape[2], k_cache.data_ptr(),
-             v_cache.data_ptr(), *strides, _ptr(score_cache), code, block_table.data_ptr(),
-             max_pages, dst_block_table.data_ptr(), dst_block_table.shape[1], seq_lens.data_ptr(),
-             batch, h_kv, d, num_pages, page_size, keep, recent, idx.data_ptr(), count.data_ptr(),
-             mass_out.data_ptr(), lens.data_ptr())
+    sc, code = _codes(score_cache, num_pages, h_kv, page_size, k_cache)
+    dst, dst_pages = bt, max_pages
+    if dst_block_table is not None:
+        dst, dst_pages = _table(dst_block_table, "dst_block_table", batch, k_cache)
+    idx = _or_new(idx, "idx", (batch, h_kv, keep), k_cache)
+    count = _or_new(count, "count", (batch, h_kv), k_cache)
+    lens = _or_new(lens, "lens", (batch,), k_cache)
+    _call_on(k_cache.get_device(), "jssa_evict", m, row, *kv, *strides, sc, code, bt, max_pages, dst,
+             dst_pages, sl, batch, h_kv, d, num_pages, page_size, keep, recent, idx.data_ptr(),
+             count.data_ptr(), mo, lens.data_ptr())
     return idx, count, lens
 
 
