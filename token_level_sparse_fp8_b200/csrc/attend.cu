@@ -209,14 +209,17 @@ __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
     x[3] = ok1 ? s[3] * scale_log2 : -INFINITY;
     if (MASS) {  // scores [pair][position of the walk][G]
       float* sc = a.scores + ((int64_t)pair * a.score_span + j_begin + j0) * G;
-      const int h0 = 2 * t, h1 = 2 * t + 1;
-      if (j0 + g < n_mine) {
-        if (h0 < G) sc[g * G + h0] = x[0];
-        if (h1 < G) sc[g * G + h1] = x[1];
-      }
-      if (j0 + g + 8 < n_mine) {
-        if (h0 < G) sc[(g + 8) * G + h0] = x[2];
-        if (h1 < G) sc[(g + 8) * G + h1] = x[3];
+      const int h0 = 2 * t;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float* to = sc + (g + 8 * u) * G + h0;
+        if (h0 >= G || j0 + g + 8 * u >= n_mine) continue;
+        if (G & 1) {
+          to[0] = x[2 * u];
+          if (h0 + 1 < G) to[1] = x[2 * u + 1];
+        } else {
+          *reinterpret_cast<float2*>(to) = make_float2(x[2 * u], x[2 * u + 1]);
+        }
       }
     }
     float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
@@ -440,22 +443,47 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttendArgs a, int sp
     lo = a.window > 0 ? max(0, L - a.window) : 0;
     n = L - lo;
   }
-  for (int j = blockIdx.x * kMassSpan + tid; j < n; j += kMassThreads) {
-    if (j >= (blockIdx.x + 1) * kMassSpan) break;
-    const float* x = a.scores + ((int64_t)pair * a.score_span + j) * G;
-    float w = 0.f;
-    bool any = false;
-    for (int g = 0; g < G; ++g) {
-      const float xg = x[g];
-      if (xg != -INFINITY) {
-        w += fast_exp2(xg - s_m[g]) * s_inv[g];
-        any = true;
-      }
+  // kMassSpan / kMassThreads positions per thread, their loads in flight together
+  constexpr int kPer = kMassSpan / kMassThreads;
+  constexpr int kG = GV > 0 ? GV : kAttendMaxG;
+  float x[kPer][kG], sum[kPer];
+  int pos[kPer];
+  float* mass = a.mass + (int64_t)pair * a.mass_stride;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int j = blockIdx.x * kMassSpan + u * kMassThreads + tid;
+    pos[u] = -1;
+    if (j >= n) continue;
+    pos[u] = INDEXED ? a.idx[(int64_t)pair * a.budget + j] : lo + j;
+    const float* src = a.scores + ((int64_t)pair * a.score_span + j) * G;
+    if (GV % 4 == 0 && GV > 0) {
+#pragma unroll
+      for (int g = 0; g < GV; g += 4) *reinterpret_cast<float4*>(&x[u][g]) = *reinterpret_cast<const float4*>(src + g);
+    } else if (GV == 2) {
+      *reinterpret_cast<float2*>(&x[u][0]) = *reinterpret_cast<const float2*>(src);
+    } else {
+#pragma unroll
+      for (int g = 0; g < kG; ++g) x[u][g] = g < G ? src[g] : -INFINITY;
     }
-    if (!any) continue;  // an unusable page or position (flagged by the first kernel)
-    const int pos = INDEXED ? a.idx[(int64_t)pair * a.budget + j] : lo + j;
-    a.mass[(int64_t)pair * a.mass_stride + pos] += w;
   }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    // an unusable page or position (flagged by the first kernel) has scores of -inf
+    bool any = false;
+    float w = 0.f;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      if (GV == 0 && g >= G) break;
+      if (x[u][g] == -INFINITY) continue;
+      w += fast_exp2(x[u][g] - s_m[g]) * s_inv[g];
+      any = true;
+    }
+    if (!any) pos[u] = -1;
+    if (pos[u] >= 0) sum[u] = mass[pos[u]] + w;
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u)
+    if (pos[u] >= 0) mass[pos[u]] = sum[u];
 }
 
 template <bool INDEXED>
