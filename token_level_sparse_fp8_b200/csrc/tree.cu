@@ -18,10 +18,10 @@
 //     stages, as 64-dimension column blocks with the 128-byte swizzle: the K-major operand of
 //     S = Q K^T and the MN-major operand of O += P V. They run ahead over pair boundaries. The
 //     nodes' rows come from k_new when given; another warp writes them to the cache.
-//   * One warp issues the MMAs. Groups of 4 warps, one thread per query row (tensor-memory lane):
-//     S from tensor memory, online softmax in registers (fp32, lazy rescale of O), P as bf16 back
-//     to tensor memory as the A operand of P V. S of the next tile is computed while the softmax of
-//     this one runs. At d = 128 two groups: both halves of 256 rows (Q of the second one in shared
+//   * Groups of 4 warps, one thread per query row (tensor-memory lane): S from tensor memory, online
+//     softmax in registers (fp32, lazy rescale of O), P as bf16 back to tensor memory as the A
+//     operand of P V. A further warp per group issues its MMAs; S of the next tile is computed while
+//     the softmax of this one runs. At d = 128 two groups: both halves of 256 rows (Q of the second one in shared
 //     memory: tensor memory is full), or, with at most 128 rows, the even and the odd tiles of the
 //     same rows, whose O are merged at the end through tensor memory (the two groups' warps share
 //     lanes). At d = 256 O takes 256 columns and one group remains.
@@ -51,13 +51,16 @@ constexpr int kCopiers = 128;  // threads that copy rows: 16 of a tile per warp
 constexpr int kBatch = 4;
 constexpr float kRescaleSlack = 8.f;  // log2 units
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kMinTiles = 2;  // tiles per CTA, before more CTAs take part
+// A branch that the tile loop hardly ever takes: its code is laid out away from the loop's.
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
+
+constexpr int kMinTiles = 4;  // tiles per CTA, before more CTAs take part
 
 template <int D, bool TWO>
 struct Cfg {
   static constexpr int kGroups = D == 128 ? 2 : 1;
   static constexpr bool kHalves = kGroups == 2 && !TWO;  // the groups share rows and split the tiles
-  // + a warpgroup of which one warp issues the MMAs and one stores the new rows
+  // + a warpgroup of which a warp per group issues its MMAs and one stores the new rows
   static constexpr int kThreads = kGroups * kM + kCopiers + 128;
   // registers per thread of the softmax, copy and MMA warpgroups; they add up to the launch's
   // (65536 / kThreads, a multiple of 8, per thread)
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
       tc::mbar_init(smem_u32(&s_empty[i]), TWO ? 2 : 1);
     }
     for (int i = 0; i < kBars * kGroups + 1; ++i)
-      tc::mbar_init(smem_u32(&s_bar[i]), i == kBars * kGroups || i % kBars < kBarFree ? 1 : 4);
+      tc::mbar_init(smem_u32(&s_bar[i]), i == kBars * kGroups ? kGroups : i % kBars < kBarFree ? 1 : 4);
     tc::fence_mbar_init();
   }
   if (warp == 0) {
@@ -275,75 +278,79 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
 
   if (warp >= kGroups * 4 + 4) {
     tc::regs_dec<C::kRegsIssue>();
-    if (warp == kGroups * 4 + 4) {
-      // ---- MMA issue: all lanes run the loop, one issues -------------------------------------------
-      // Items in order: (tile, group) with rows of their own, tiles of alternating groups otherwise.
-      // The S of a group's next item goes before the P V of this one.
+    if (warp < kGroups * 4 + 4 + kGroups) {
+      // ---- MMA issue, a warp per group: all lanes run the loop, one issues --------------------------
+      // The S of the group's next tile goes before the P V of this one, under whose softmax it is
+      // computed. The warp sleeps in its waits: one that polls takes issue slots from the softmax.
+      const int g = warp - (kGroups * 4 + 4);
       constexpr uint32_t kIdescS = tc::idesc_bf16(kM, kTT, false);
       constexpr uint32_t kIdescO = tc::idesc_bf16(kM, D, true);
-      constexpr int kStride = kHalves ? 2 : 1;  // tiles from one item of a group to its next
+      constexpr int kStride = kHalves ? 2 : 1;  // tiles from one tile of the group to its next
       const uint32_t on = tc::elect_one();
-      uint32_t n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_q = 0;  // S, P V and segments so far
-      auto bar = [&](int g, int which) { return smem_u32(&s_bar[kBars * g + which]); };
+      auto bar = [&](int which) { return smem_u32(&s_bar[kBars * g + which]); };
       auto wait = [&](uint32_t b, uint32_t parity) {  // (the whole warp agrees)
-        if (!fail) fail = __any_sync(kAll, !tc::mbar_wait(b, parity, limit));
+        if (!fail) fail = __any_sync(kAll, !tc::mbar_wait(b, parity & 1u, limit));
       };
-      auto stage_of = [&](int64_t k) { return ring + (uint32_t)(k % C::kStages) * C::kStageBytes; };
-      auto issue_s = [&](int g, int64_t k) {
-        if (n_s[g] > 0) wait(bar(g, kBarFree), (n_s[g] - 1) & 1);
-        ++n_s[g];
-        wait(smem_u32(&s_full[k % C::kStages]), (uint32_t)((k / C::kStages) & 1));
-        if (fail) return;
-        // the rows came by cp.async (generic proxy); the tensor cores read through the async proxy
-        tc::fence_proxy_async_smem();
-        tc::fence_after_sync();
-        const uint32_t ts = tmem + C::kS + g * kTT;
-        const uint64_t b0 = tc::sw128_desc(stage_of(k), 16, 1024);
-        if (TWO && g == 1) {
-          const uint64_t a0 = tc::sw128_desc(q_smem, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ss_warp(on, ts, a0 + (uint64_t)(((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4),
-                            b0 + (uint64_t)(((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4),
-                            kIdescS, kk > 0);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ts_warp(on, ts, tmem + C::kQ + kk * 8,
-                            b0 + (uint64_t)(((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4),
-                            kIdescS, kk > 0);
-        }
-        tc::mma_commit_warp(on, bar(g, kBarS));
-      };
+      const uint32_t ts = tmem + C::kS + g * kTT, tp = tmem + C::kP + g * (kTT / 2), to = tmem + C::kO + g * D;
+      uint32_t n_s = 0, n_p = 0, n_q = 0;  // S and P V issued, segments
       int64_t k0 = 0;
-      while (k0 < todo) {
+      while (k0 < todo && !fail) {
         const int tiles = pair_of(a, pair).tiles;
         const int n = (int)min((int64_t)tiles - t0, todo - k0);  // tiles of the segment
-        for (int g = 0; g < kGroups; ++g) {
-          if (kHalves ? g == 0 : true) wait(bar(g, kBarQ), n_q & 1);
-          if (!kHalves || g < n) issue_s(g, k0 + (kHalves ? g : 0));
-        }
-        ++n_q;
-        for (int i = 0; i < n; ++i) {
+        int i_s = kHalves ? g : 0;  // the next S, with its stage
+        int st_s = (int)((k0 + i_s) % C::kStages), st_p = st_s;
+        uint32_t lap = (uint32_t)((k0 + i_s) / C::kStages);
+        auto issue_s = [&]() {
+          if (n_s > 0) wait(bar(kBarFree), n_s - 1);
+          wait(smem_u32(&s_full[st_s]), lap);
+          if (fail) return;
+          // the rows came by cp.async (generic proxy); the tensor cores read by the async proxy
+          tc::fence_proxy_async_smem();
+          tc::fence_after_sync();
+          const uint64_t b0 = tc::sw128_desc(ring + st_s * C::kStageBytes, 16, 1024);
+          const uint64_t a0 = tc::sw128_desc(q_smem, 16, 1024);
+          if (TWO && g == 1) {
 #pragma unroll
-          for (int gg = 0; gg < (kHalves ? 1 : kGroups); ++gg) {
-            const int g = kHalves ? i & 1 : gg;
-            const int64_t k = k0 + i;
-            if (i + kStride < n) issue_s(g, k + kStride);
-            wait(bar(g, kBarP), n_p[g] & 1);
-            ++n_p[g];
-            if (fail) continue;
-            tc::fence_after_sync();
-            const uint32_t tp = tmem + C::kP + g * (kTT / 2), to = tmem + C::kO + g * D;
-            const uint64_t b0 = tc::sw128_desc(stage_of(k) + C::kTileBytes, C::kBlockBytes, 1024);
-            const bool more = *(volatile uint32_t*)&s_keep[g] != 0u;
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_ss_warp(on, ts, a0 + (uint64_t)(((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4),
+                              b0 + (uint64_t)(((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4),
+                              kIdescS, kk > 0);
+          } else {
 #pragma unroll
-            for (int kk = 0; kk < kTT / 16; ++kk)
-              tc::mma_ts_warp(on, to, tp + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
-                              more || kk > 0);
-            tc::mma_commit_warp(on, bar(g, kBarO));
-            tc::mma_commit_warp(on, smem_u32(&s_empty[k % C::kStages]));
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_ts_warp(on, ts, tmem + C::kQ + kk * 8,
+                              b0 + (uint64_t)(((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4),
+                              kIdescS, kk > 0);
           }
+          tc::mma_commit_warp(on, bar(kBarS));
+          ++n_s;
+          i_s += kStride;
+          st_s += kStride;
+          if (st_s >= C::kStages) {
+            st_s -= C::kStages;
+            ++lap;
+          }
+        };
+        wait(smem_u32(&s_bar[kBars * (kHalves ? 0 : g) + kBarQ]), n_q);
+        ++n_q;
+        if (i_s < n) issue_s();
+        for (int i = kHalves ? g : 0; i < n && !fail; i += kStride) {
+          if (i_s < n) issue_s();
+          wait(bar(kBarP), n_p);
+          if (fail) break;
+          tc::fence_after_sync();
+          const uint64_t b0 = tc::sw128_desc(ring + st_p * C::kStageBytes + C::kTileBytes,
+                                             C::kBlockBytes, 1024);
+          const bool add = *(volatile uint32_t*)&s_keep[g] != 0u;
+#pragma unroll
+          for (int kk = 0; kk < kTT / 16; ++kk)
+            tc::mma_ts_warp(on, to, tp + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
+                            add || kk > 0);
+          tc::mma_commit_warp(on, bar(kBarO));
+          tc::mma_commit_warp(on, smem_u32(&s_empty[st_p]));
+          ++n_p;
+          st_p += kStride;
+          if (st_p >= C::kStages) st_p -= C::kStages;
         }
         k0 += n;
         t0 = 0;
@@ -352,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
       // everything issued has completed before the tensor memory is freed
       tc::mma_commit_warp(on, smem_u32(&s_bar[kBars * kGroups]));
       if (!tc::mbar_wait(smem_u32(&s_bar[kBars * kGroups]), 0)) fail = true;
-    } else if (warp == kGroups * 4 + 5 && rg == 0) {
+    } else if (warp == kGroups * 4 + 4 + kGroups && rg == 0) {
       // ---- bad lengths and parents are reported, the new nodes' rows written to the cache -----------
       const int max_len = a.max_pages * a.page_size;
       for (int64_t k0 = 0; k0 < todo;) {
@@ -600,31 +607,36 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
 #pragma unroll 1
       for (int t = t0 + (kHalves ? g : 0); t < t1; t += kHalves ? 2 : 1) {
         const uint32_t stage = ring + st * C::kStageBytes;
-        if (!fail) fail = !tc::mbar_wait(bar(kBarS), n_t & 1, limit);
+        // S of this tile; its rows' validity (they are in long since, when S is: the tests overlap)
+        {
+          const bool s_in = tc::mbar_test(bar(kBarS), n_t & 1);
+          const bool rows_in = tc::mbar_test(smem_u32(&s_full[st]), lap & 1);
+          if (rare(!s_in) && !fail) fail = !tc::mbar_wait(bar(kBarS), n_t & 1, limit);
+          if (rare(!rows_in) && !fail) fail = !tc::mbar_wait(smem_u32(&s_full[st]), lap & 1, limit);
+        }
         tc::fence_after_sync();
         uint32_t s0[32], s1[32];
         if (active) {
           tc::tmem_ld32(ts, s0);
           tc::tmem_ld32(ts + 32, s1);
         }
-        // (S is there, so the rows are: this wait only makes s_valid visible)
-        if (!fail) fail = !tc::mbar_wait(smem_u32(&s_full[st]), lap & 1, limit);
-        // the list indexes of this tile that the row sees
-        uint64_t see_t = s_valid[st];
+        uint64_t see_t = s_valid[st];  // the list indexes of this tile that the row sees
         const int j0 = t * kTT, c_left = p.n_ctx - j0;  // context positions from here on
-        if (c_left < kTT) {
-          const uint64_t ctx = c_left > 0 ? (1ull << c_left) - 1ull : 0ull;
-          const uint64_t tr = c_left >= 0 ? see << c_left : (-c_left < 64 ? see >> -c_left : 0ull);
-          see_t &= ctx | tr;
-        }
-        if (lo > j0) see_t &= lo - j0 < 64 ? ~0ull << (lo - j0) : 0ull;
-        if (!used) see_t = ~0ull;  // (its row is discarded)
         // uniform over the CTA: some row may mask a position that is in the tile
         const bool special = c_left < kTT || (a.window > 0 && t == 0);
+        if (rare(special)) {
+          if (c_left < kTT) {
+            const uint64_t ctx = c_left > 0 ? (1ull << c_left) - 1ull : 0ull;
+            const uint64_t tr = c_left >= 0 ? see << c_left : (-c_left < 64 ? see >> -c_left : 0ull);
+            see_t &= ctx | tr;
+          }
+          if (lo > j0) see_t &= lo - j0 < 64 ? ~0ull << (lo - j0) : 0ull;
+          if (!used) see_t = ~0ull;  // (its row is discarded)
+        }
         if (active) tc::tmem_wait_ld();
         arrive(kBarFree);
         if (active) {
-          if (!__all_sync(kAll, see_t == ~0ull)) {
+          if (rare(!__all_sync(kAll, see_t == ~0ull))) {
             const uint32_t lo32 = (uint32_t)see_t, hi32 = (uint32_t)(see_t >> 32);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -646,10 +658,16 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
           const bool grow = mt > m_ref + kRescaleSlack;
           const float m_new = grow ? mt : m_ref;
           const float corr = grow && m_ref != -INFINITY ? fast_exp2(m_ref - m_new) : 1.f;
-          // P V of the group's previous tile: done with P and O
-          if (n_t > 0 && !fail) fail = !tc::mbar_wait(bar(kBarO), (n_t - 1) & 1, limit);
-          tc::fence_after_sync();
-          if (have_o && __any_sync(kAll, corr != 1.f)) {
+          // P V of the group's previous tile: done with P and O (tested here, its latency under the
+          // exponentials)
+          bool o_done = n_t == 0 || tc::mbar_test(bar(kBarO), (n_t - 1) & 1);
+          auto previous_done = [&]() {
+            if (rare(!o_done) && !fail) fail = !tc::mbar_wait(bar(kBarO), (n_t - 1) & 1, limit);
+            o_done = true;
+            tc::fence_after_sync();
+          };
+          if (rare(have_o && __any_sync(kAll, corr != 1.f))) {
+            previous_done();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -662,23 +680,24 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
           }
           m_ref = m_new;
           const float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
-          float sum[2] = {0.f, 0.f};
+          const float2 sc2 = make_float2(scale_log2, scale_log2), ms2 = make_float2(-m_sub, -m_sub);
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+          uint32_t ph[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t ph[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float x0 = __uint_as_float(h ? s1[2 * j] : s0[2 * j]);
-              const float x1 = __uint_as_float(h ? s1[2 * j + 1] : s0[2 * j + 1]);
-              const float p0 = fast_exp2(fmaf(x0, scale_log2, -m_sub));
-              const float p1 = fast_exp2(fmaf(x1, scale_log2, -m_sub));
-              sum[0] += p0;
-              sum[1] += p1;
-              ph[j] = pack_bf16x2(p0, p1);
-            }
-            tc::tmem_st16(tp + 16 * h, ph);
+          for (int j = 0; j < 32; ++j) {
+            float2 p = j < 16 ? make_float2(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1]))
+                              : make_float2(__uint_as_float(s1[2 * j - 32]), __uint_as_float(s1[2 * j - 31]));
+            p = fma2(p, sc2, ms2);
+            p.x = fast_exp2(p.x);
+            p.y = fast_exp2(p.y);
+            if (j & 1) sum1 = add2(sum1, p);
+            else sum0 = add2(sum0, p);
+            ph[j] = pack_bf16x2(p.x, p.y);
           }
-          l = l * corr + (sum[0] + sum[1]);
+          sum0 = add2(sum0, sum1);
+          l = l * corr + (sum0.x + sum0.y);
+          previous_done();
+          tc::tmem_st32(tp, ph);
           tc::tmem_wait_st();
         } else {
           // (keeps this warp's arrivals in step: P of the previous tile has been taken)
@@ -686,7 +705,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
           tc::fence_after_sync();
         }
         bool keep_o = have_o;
-        if (special) {
+        if (rare(special)) {
           // this thread's half row of V: any exponent of all ones
           const uint32_t vrow = stage + C::kTileBytes + (gt >> 1) * 128;
           constexpr int kPer = D / 16;  // 16-byte chunks of half a row
@@ -746,6 +765,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
               }
               tc::tmem_st32(to + 32 * c, o);
             }
+            tc::tmem_wait_st();
             keep_o = true;
             tc::bar_sync(vbar, vthreads);  // everyone has read V
             if (!TWO || g == 0) {          // clear the elements for the MMA
@@ -767,8 +787,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
         }
         // (thread 0 of the group also says whether P V adds to O: the same for all its tiles but the
         // first, and but for the slow path above)
-        if (gt == 0) *(volatile uint32_t*)&s_keep[g] = keep_o;
-        tc::tmem_wait_st();
+        if (rare(t < t0 + 2 * (kHalves ? 2 : 1) || special) && gt == 0) *(volatile uint32_t*)&s_keep[g] = keep_o;
         arrive(kBarP);
         have_o = true;
         ++n_t;
