@@ -886,9 +886,11 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
 
 // Merge of the pairs that several CTAs share,
 //   M = max m_i,  w_i = 2^(m_i - M),  out = sum w_i O_i / sum w_i l_i.
-// Block (x, y): the pair in whose middle CTA x begins, if it is the first such CTA, and 32 of its
-// rows, 4 per warp (their loads in flight together).
-constexpr int kMergeWarps = 8, kMergeRows = 4;
+// Block (x, y): the pair in whose middle CTA x begins, if it is the first such CTA, and 8 of its rows,
+// one per warp. Latency-bound: the (m, l) and O of kMergeParts partials are read at once, and the weights
+// applied as they come (a running maximum). One row per warp keeps all blocks resident at once: with 4
+// (126 registers) the merge of 148 x 256 rows took 12 us longer.
+constexpr int kMergeWarps = 8, kMergeParts = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     merge_kernel(TreeArgs a, int row_groups, int group_rows, int slot_rows, int ctas) {
@@ -896,86 +898,77 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int x = blockIdx.x / row_groups + 1, rg = blockIdx.x % row_groups, n_cta = ctas / row_groups;
   const Work ws = work_of(a.ws, ctas, slot_rows);
   pdl_wait();
-  const int2 at = ws.at[x], before = ws.at[x - 1];
-  if (at.x < 0 || at.y == 0) return;                      // CTA x begins at a pair's first tile
-  if (before.x == at.x && before.y > 0) return;           // an earlier CTA begins inside the pair, too
-  const int pair = at.x, G = a.h_q / a.h_kv, rows = a.n * G;
+  // lane i: where CTA x - 1 + i begins
+  const int2 at = x - 1 + lane < n_cta ? ws.at[x - 1 + lane] : make_int2(-1, 0);
+  const int pair = __shfl_sync(kAll, at.x, 1);
+  const bool inside = at.x == pair && at.y > 0;  // it begins in the middle of the pair
+  unsigned in = __ballot_sync(kAll, inside);
+  if (pair < 0 || !(in & 2u) || (in & 1u)) return;  // CTA x is not the first that does
+  const int first = __shfl_sync(kAll, at.x, 0) == pair ? 0 : 1;
   // partial 0: CTA x - 1's last segment; partial i > 0: the first segment of CTA x - 1 + i
-  int parts = 2;
-  for (int y = x + 1; y < n_cta; y += 32) {
-    const int2 more = y + lane < n_cta ? ws.at[y + lane] : make_int2(-1, 0);
-    const unsigned in = __ballot_sync(kAll, more.x == pair && more.y > 0);
-    parts += in == kAll ? 32 : __ffs(~in) - 1;
-    if (in != kAll) break;
+  int parts = __ffs(~(in | 1u)) - 1;
+  if (parts < 0) {
+    parts = 32;
+    for (int y = x + 31; y < n_cta; y += 32) {
+      const int2 more = y + lane < n_cta ? ws.at[y + lane] : make_int2(-1, 0);
+      in = __ballot_sync(kAll, more.x == pair && more.y > 0);
+      parts += in == kAll ? 32 : __ffs(~in) - 1;
+      if (in != kAll) break;
+    }
   }
-  const int first = before.x == pair ? 0 : 1;
   auto slot_of = [&](int i) {
     return (int64_t)(2 * ((x - 1 + i) * row_groups + rg) + (i == 0 ? first : 0)) * slot_rows;
   };
-  int lr[kMergeRows];
-  float M[kMergeRows], l[kMergeRows], acc[kMergeRows][D / 32];
+  const int G = a.h_q / a.h_kv, rows = a.n * G;
+  const int lr = blockIdx.y * kMergeWarps + warp, r = rg * group_rows + lr;
+  if (lr >= slot_rows || r >= rows) return;
+  float M = -INFINITY, l = 0.f, acc[D / 32];
 #pragma unroll
-  for (int u = 0; u < kMergeRows; ++u) {
-    lr[u] = (blockIdx.y * kMergeWarps + warp) * kMergeRows + u;
-    if (lr[u] >= slot_rows) lr[u] = slot_rows - 1;  // (computed twice, written once)
-    M[u] = -INFINITY;
-    l[u] = 0.f;
+  for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < parts; i0 += kMergeParts) {
+    float2 ml[kMergeParts];
+    float4 o[kMergeParts][D / 128];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[u][e] = 0.f;
-  }
-  for (int i = lane; i < parts; i += 32)
+    for (int i = 0; i < kMergeParts; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i >= parts) continue;
+      const int64_t row = slot_of(i0 + i) + lr;
+      ml[i] = __ldcg(ws.ml + row);
 #pragma unroll
-    for (int u = 0; u < kMergeRows; ++u) M[u] = fmaxf(M[u], ws.ml[slot_of(i) + lr[u]].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-#pragma unroll
-    for (int u = 0; u < kMergeRows; ++u) M[u] = fmaxf(M[u], __shfl_xor_sync(kAll, M[u], o));
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float w[kMergeRows];
-#pragma unroll
-    for (int u = 0; u < kMergeRows; ++u) {
-      w[u] = 0.f;
-      if (i0 + lane < parts) {
-        const float2 ml = ws.ml[slot_of(i0 + lane) + lr[u]];
-        w[u] = merge_weight(ml.x, ml.y, M[u]);
-        if (w[u] != 0.f) l[u] += w[u] * ml.y;
-      }
+      for (int q = 0; q < D / 128; ++q)
+        o[i][q] = __ldcg(reinterpret_cast<const float4*>(ws.o + row * D) + q * 32 + lane);
     }
-    const int m = min(32, parts - i0);
-#pragma unroll 2
-    for (int i = 0; i < m; ++i) {
+    float top = M;
 #pragma unroll
-      for (int u = 0; u < kMergeRows; ++u) {
-        const float wi = __shfl_sync(kAll, w[u], i);
-        const float4* o = reinterpret_cast<const float4*>(ws.o + (slot_of(i0 + i) + lr[u]) * D);
+    for (int i = 0; i < kMergeParts; ++i) top = fmaxf(top, ml[i].x);
+    const float keep = M == -INFINITY ? 1.f : fast_exp2(M - top);  // (of zeros, or of NaN sums)
+    M = top;
+    l *= keep;
 #pragma unroll
-        for (int q = 0; q < D / 128; ++q) {
-          const float4 v = o[q * 32 + lane];
-          if (wi != 0.f) {
-            acc[u][4 * q] += wi * v.x;
-            acc[u][4 * q + 1] += wi * v.y;
-            acc[u][4 * q + 2] += wi * v.z;
-            acc[u][4 * q + 3] += wi * v.w;
-          }
-        }
+    for (int e = 0; e < D / 32; ++e) acc[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < kMergeParts; ++i) {
+      const float w = merge_weight(ml[i].x, ml[i].y, top);
+      if (w == 0.f) continue;
+      l += w * ml[i].y;
+#pragma unroll
+      for (int q = 0; q < D / 128; ++q) {
+        acc[4 * q] += w * o[i][q].x;
+        acc[4 * q + 1] += w * o[i][q].y;
+        acc[4 * q + 2] += w * o[i][q].z;
+        acc[4 * q + 3] += w * o[i][q].w;
       }
     }
   }
   const int b = pair / a.h_kv, h = pair % a.h_kv;
+  const float inv = inverse_sum(l);
+  uint16_t* out = a.out + (((int64_t)b * a.n + r / G) * a.h_q + (int64_t)h * G + r % G) * D;
 #pragma unroll
-  for (int u = 0; u < kMergeRows; ++u) {
-    float s = l[u];
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    const float inv = inverse_sum(s);
-    const int row = (blockIdx.y * kMergeWarps + warp) * kMergeRows + u, r = rg * group_rows + row;
-    if (row >= slot_rows || r >= rows) continue;
-    uint16_t* out = a.out + (((int64_t)b * a.n + r / G) * a.h_q + (int64_t)h * G + r % G) * D;
-#pragma unroll
-    for (int q = 0; q < D / 128; ++q)
-      reinterpret_cast<uint2*>(out)[q * 32 + lane] =
-          make_uint2(pack_bf16x2(acc[u][4 * q] * inv, acc[u][4 * q + 1] * inv),
-                     pack_bf16x2(acc[u][4 * q + 2] * inv, acc[u][4 * q + 3] * inv));
-  }
+  for (int q = 0; q < D / 128; ++q)
+    reinterpret_cast<uint2*>(out)[q * 32 + lane] =
+        make_uint2(pack_bf16x2(acc[4 * q] * inv, acc[4 * q + 1] * inv),
+                   pack_bf16x2(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
 }
 
 template <int D, bool TWO>
@@ -997,8 +990,7 @@ cudaError_t launch_t(const TreeArgs& a, const Plan& plan, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, kern, a, plan.row_groups, plan.slot_rows, tc_wait_limit());
   if (e != cudaSuccess) return e;
   if (plan.ctas == plan.row_groups) return cudaGetLastError();  // one CTA has every pair whole
-  cfg.gridDim = dim3(plan.ctas - plan.row_groups,
-                     (plan.slot_rows + kMergeWarps * kMergeRows - 1) / (kMergeWarps * kMergeRows), 1);
+  cfg.gridDim = dim3(plan.ctas - plan.row_groups, (plan.slot_rows + kMergeWarps - 1) / kMergeWarps, 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, plan.row_groups, plan.group_rows, plan.slot_rows,
