@@ -391,47 +391,21 @@ __global__ void __launch_bounds__(kThreads, Ring<D>::kCtasPerSm)
 // attended position's weight to its running sum,
 //   mass[pair][t] += sum_g 2^(x_g(t) - M_g) / l_g,
 // with M_g, l_g the merged maximum and sum of query head g. Grid (position blocks, pairs); every
-// block re-reads the pair's few (m, l). All sums in fp32.
+// block re-reads the pair's few (m, l). All sums in fp32. It moves 4 G + 8 bytes per position, little
+// beside the 4 d of the first kernel, and is latency-bound: the scores and the old sums are on their
+// way while the partials' maxima are merged.
 constexpr int kMassThreads = 256;
-constexpr int kMassSpan = 1024;  // positions per block
+constexpr int kMassSpan = 1024;    // positions per block
+constexpr int kMassSplits = 128;   // splits whose weights are kept in shared memory
 
 template <int GV, bool INDEXED>
 __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttendArgs a, int splits) {
-  __shared__ float s_m[kAttendMaxG], s_inv[kAttendMaxG];
+  __shared__ float s_m[kAttendMaxG], s_inv[kAttendMaxG], s_w[kAttendMaxG][kMassSplits];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pair = blockIdx.y, b = pair / a.h_kv;
   const int G = GV > 0 ? GV : a.h_q / a.h_kv;
   const int row_f = part_row(a.d);
   pdl_wait();
-  const float* part = reinterpret_cast<const float*>(a.ws) + (int64_t)pair * splits * G * row_f;
-  if (warp < G) {
-    float m = -INFINITY;
-    for (int sp = lane; sp < splits; sp += 32) m = fmaxf(m, part[((int64_t)sp * G + warp) * row_f]);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
-    if (m != -INFINITY)
-      for (int sp = lane; sp < splits; sp += 32) {
-        const float* p = part + ((int64_t)sp * G + warp) * row_f;
-        l += fast_exp2(p[0] - m) * p[1];
-      }
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_inv[warp] = l > 0.f ? 1.f / l : 0.f;
-    }
-  }
-  __syncthreads();
-  // this block's share of the output elements
-  for (int e = blockIdx.x * kMassThreads + tid; e < G * a.d; e += gridDim.x * kMassThreads) {
-    const int g = e / a.d, dim = e % a.d;
-    float acc = 0.f;
-    if (s_m[g] != -INFINITY)
-      for (int sp = 0; sp < splits; ++sp) {
-        const float* p = part + ((int64_t)sp * G + g) * row_f;
-        acc += fast_exp2(p[0] - s_m[g]) * p[2 + dim];
-      }
-    a.out[(int64_t)pair * G * a.d + e] = f_to_bf16(acc * s_inv[g]);
-  }
   int n, lo = 0;
   if (INDEXED) {
     n = a.count[pair];
@@ -443,18 +417,25 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttendArgs a, int sp
     lo = a.window > 0 ? max(0, L - a.window) : 0;
     n = L - lo;
   }
-  // kMassSpan / kMassThreads positions per thread, their loads in flight together
+  // kMassSpan / kMassThreads positions per thread
   constexpr int kPer = kMassSpan / kMassThreads;
   constexpr int kG = GV > 0 ? GV : kAttendMaxG;
   float x[kPer][kG], sum[kPer];
   int pos[kPer];
   float* mass = a.mass + (int64_t)pair * a.mass_stride;
+  const int src_len = a.max_pages * a.page_size;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     const int j = blockIdx.x * kMassSpan + u * kMassThreads + tid;
-    pos[u] = -1;
-    if (j >= n) continue;
-    pos[u] = INDEXED ? a.idx[(int64_t)pair * a.budget + j] : lo + j;
+    pos[u] = j < n ? (INDEXED ? a.idx[(int64_t)pair * a.budget + j] : lo + j) : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int j = blockIdx.x * kMassSpan + u * kMassThreads + tid;
+    if (pos[u] < 0 || pos[u] >= src_len) {  // (none, or flagged by the first kernel)
+      pos[u] = -1;
+      continue;
+    }
     const float* src = a.scores + ((int64_t)pair * a.score_span + j) * G;
     if (GV % 4 == 0 && GV > 0) {
 #pragma unroll
@@ -465,25 +446,56 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttendArgs a, int sp
 #pragma unroll
       for (int g = 0; g < kG; ++g) x[u][g] = g < G ? src[g] : -INFINITY;
     }
+    sum[u] = mass[pos[u]];
   }
+  // the merged maximum and sum of query head `warp`
+  const float* part = reinterpret_cast<const float*>(a.ws) + (int64_t)pair * splits * G * row_f;
+  if (warp < G) {
+    const float* p = part + (int64_t)warp * row_f;
+    const int64_t step = (int64_t)G * row_f;
+    float m = -INFINITY;
+    for (int sp = lane; sp < splits; sp += 32) m = fmaxf(m, p[sp * step]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    for (int sp = lane; sp < splits; sp += 32) {
+      const float w = m != -INFINITY ? fast_exp2(p[sp * step] - m) : 0.f;
+      if (sp < kMassSplits) s_w[warp][sp] = w;
+      l += w * p[sp * step + 1];
+    }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_inv[warp] = l > 0.f ? 1.f / l : 0.f;
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    // an unusable page or position (flagged by the first kernel) has scores of -inf
-    bool any = false;
+    if (pos[u] < 0) continue;
+    // an unusable page (flagged by the first kernel) has scores of -inf and adds nothing
     float w = 0.f;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       if (GV == 0 && g >= G) break;
-      if (x[u][g] == -INFINITY) continue;
-      w += fast_exp2(x[u][g] - s_m[g]) * s_inv[g];
-      any = true;
+      if (x[u][g] != -INFINITY) w += fast_exp2(x[u][g] - s_m[g]) * s_inv[g];
     }
-    if (!any) pos[u] = -1;
-    if (pos[u] >= 0) sum[u] = mass[pos[u]] + w;
+    mass[pos[u]] = sum[u] + w;
   }
-#pragma unroll
-  for (int u = 0; u < kPer; ++u)
-    if (pos[u] >= 0) mass[pos[u]] = sum[u];
+  // this block's share of the output elements
+  for (int e = blockIdx.x * kMassThreads + tid; e < G * a.d; e += gridDim.x * kMassThreads) {
+    const int g = e / a.d, dim = e - g * a.d;
+    const float* p = part + (int64_t)g * row_f;
+    const int64_t step = (int64_t)G * row_f;
+    float acc = 0.f;
+    if (s_m[g] != -INFINITY) {
+      const int near = min(splits, kMassSplits);
+#pragma unroll 8
+      for (int sp = 0; sp < near; ++sp) acc += s_w[g][sp] * p[sp * step + 2 + dim];
+      for (int sp = kMassSplits; sp < splits; ++sp)
+        acc += fast_exp2(p[sp * step] - s_m[g]) * p[sp * step + 2 + dim];
+    }
+    a.out[(int64_t)pair * G * a.d + e] = f_to_bf16(acc * s_inv[g]);
+  }
 }
 
 template <bool INDEXED>
