@@ -112,7 +112,8 @@ JSSA_API int jssa_version(void);
 
 /*
  * Debug control (the pages have no counterpart): the clock-cycle limit of each wait on the tensor
- * cores inside the tile loop of jssa_mla_attend (default 2e9 cycles, about one second at the
+ * cores inside the tile loop of jssa_mla_attend, and of each wait between the warps of
+ * jssa_tree_attend (default 2e9 cycles, about one second at the
  * boost clock). A wait that runs out raises JSSA_DEVERR_TIMEOUT in the device error word; the
  * CTA then waits, with the default limit, for every tensor-core operation it issued, frees its
  * tensor memory and returns, so the context stays usable and the next call runs normally (its
@@ -473,8 +474,8 @@ JSSA_API int jssa_evict(const float* mass, int64_t mass_stride, jssa_bf16* k_cac
  * tokens (the context); node i of sequence b is a token whose K / V row is at position
  * seq_lens[b] + i. parents int32 [batch, n_nodes]: -1 = the node follows the last committed token,
  * 0 <= p < i = it follows node p, below -1 = unused (padding: its output rows are zero, its cache
- * row is neither read nor written). A parent >= i, or one that names an unused node, makes the node
- * unused and raises JSSA_DEVERR_INDEX.
+ * row is not written and reaches no output). A parent >= i, or one that names an unused node, makes
+ * the node unused and raises JSSA_DEVERR_INDEX.
  *   out[b, i, hq] = softmax(softmax_scale * q[b, i, hq] K^T) V
  * over the node's context positions, itself and its ancestors. The context is every position below
  * seq_lens[b]; with window > 0 the positions above seq_len + depth - window, where the node's depth

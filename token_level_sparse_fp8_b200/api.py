@@ -806,7 +806,7 @@ def evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
 
 
 def set_wait_limit(cycles: int) -> int:
-    """Clock-cycle limit of the tensor-core waits in the latent attention's tile loop (a debug
+    """Clock-cycle limit of the waits in the tile loops of the latent and the tree attention (a debug
     control; <= 0 restores the default). Returns the previous limit."""
     return int(_lib.load().jssa_set_wait_limit(int(cycles)))
 

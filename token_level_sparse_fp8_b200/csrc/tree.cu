@@ -25,7 +25,7 @@
 //     memory: tensor memory is full), or, with at most 128 rows, the even and the odd tiles of the
 //     same rows, whose O are merged at the end through tensor memory (the two groups' warps share
 //     lanes). At d = 256 O takes 256 columns and one group remains.
-//   * P is rounded to bf16 (half a step, 2^-9 of a weight): the tensor cores take bf16 beside the
+//   * P is rounded to bf16 (half a step, at most 2^-8 of a weight): the tensor cores take bf16 beside the
 //     bf16 V; the sum l is kept from the fp32 weights.
 //   * Pairs cut between CTAs leave fp32 (m, l, O) partials; a second kernel merges them.
 // Masked positions must not reach the output even when V holds inf or NaN there (0 * inf): tiles
