@@ -803,3 +803,145 @@ def test_tree_wait_timeout_then_recovery(d, n, g):
     assert J.device_error(clear=True) & 32
     out = J.tree_attend(q, c.k, c.v, c.bt, c.seq_lens, cuda(parents), kn, vn)
     assert torch.equal(out, want) and J.device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("pages,mass_apart", [("same", True), ("other", False)])
+@pytest.mark.parametrize("batch,L,keep", [(2, 700, 150), (1, 30000, 5000)])
+def test_evict_half_in_place(pages, mass_apart, batch, L, keep):
+    # the pages move in place but not the mass, or the other way round
+    J = jssa()
+    c = Paged([1] * batch, 0, 2, 128, pages=-(-L // 16), seed=keep)
+    c.lens = [L - 30 * b for b in range(batch)]
+    lens = cuda(c.lens)
+    c.k.copy_(c.normal(*c.k.shape)), c.v.copy_(c.normal(*c.v.shape))
+    mass = torch.rand((batch, 2, c.table.shape[1] * 16), device="cuda") ** 6
+    m0, k0 = mass.clone(), c.k.clone()
+    mass_out = torch.full_like(mass, 5.0) if mass_apart else mass
+    dst, n0 = None, c.k.shape[0]
+    table = c.table
+    if pages == "other":
+        per = -(-keep // 16)
+        c.k, c.v = (torch.cat([t, torch.zeros((batch * per, *t.shape[1:]), dtype=t.dtype, device="cuda")])
+                    for t in (c.k, c.v))
+        table = n0 + np.arange(batch * per).reshape(batch, per)
+        dst = cuda(table)
+    idx, count, _ = J.evict(mass, c.k, c.v, c.bt, lens, keep, 9, dst_block_table=dst, mass_out=mass_out)
+    for b, n in enumerate(c.lens):
+        for h in range(2):
+            want = C.kept_positions(m0[b, h].cpu().numpy(), n, keep, 9)
+            assert np.array_equal(idx[b, h].cpu().numpy(), want)
+            w, i = torch.as_tensor(want).cuda(), torch.arange(keep, device="cuda")
+            to = torch.as_tensor(table[b]).cuda()[i // 16]
+            assert torch.equal(c.k[to, i % 16, h], k0[c.bt[b].long()[w // 16], w % 16, h])
+            assert torch.equal(mass_out[b, h, :keep], m0[b, h, w])
+            assert torch.count_nonzero(mass_out[b, h, keep:n]).item() == 0
+    if pages == "other":
+        assert torch.equal(c.k[:n0], k0)
+    if mass_apart:
+        assert torch.equal(mass, m0)
+    assert J.device_error() == 0
+
+
+def test_calls_at_once_on_two_streams():
+    # eager calls of every operator on two streams, each on its own data, nothing waited for
+    J = jssa()
+    cs = [Paged([900, 333], 16, 2, seed=30 + i) for i in range(2)]
+    for c in cs:
+        c.k.nan_to_num_(0.25), c.v.nan_to_num_(0.25)
+    work = []
+    for c in cs:
+        work.append(dict(q=c.normal(2, 16, 8, 128).cuda(), kn=c.normal(2, 16, 2, 128).cuda(),
+                         vn=c.normal(2, 16, 2, 128).cuda(),
+                         par=cuda([random_tree(c.rng, 16) for _ in range(2)]),
+                         path=cuda([[0, 2, 5, 9], [1, 3, 4, 15]]), n=cuda([4, 3])))
+
+    def run(c, w, mass):
+        o = [J.tree_attend(w["q"], c.k, c.v, c.bt, c.seq_lens, w["par"], w["kn"], w["vn"])]
+        lens = J.tree_commit(c.k, c.v, c.bt, c.seq_lens, w["path"], w["n"])
+        o.append(J.dense_decode(w["q"][:, 0].contiguous(), c.k, c.v, c.bt, lens, mass=mass))
+        o += list(J.evict(mass, c.k, c.v, c.bt, lens, 100, 7))
+        return o + [mass, c.k.clone(), c.v.clone()]
+
+    def fresh(c):
+        return torch.zeros((2, 2, c.table.shape[1] * 16), device="cuda")
+
+    start = [(c.k.clone(), c.v.clone()) for c in cs]
+    want = [run(c, w, fresh(c)) for c, w in zip(cs, work)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, (k, v) in zip(cs, start):
+            c.k.copy_(k), c.v.copy_(v)
+        masses = [fresh(c) for c in cs]
+        streams = [torch.cuda.Stream() for _ in cs]
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for s, c, w, m in zip(streams, cs, work, masses):
+            with torch.cuda.stream(s):
+                got.append(run(c, w, m))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert J.device_error() == 0
+
+
+def test_step_captured_and_replayed():
+    # one graph of a whole round: draft, commit, a step with its mass, an eviction
+    J = jssa()
+    lens, h_kv, g, n = [200, 90], 2, 4, 8
+    c = Paged(lens, 60, h_kv, 128, seed=40)
+    c.k.nan_to_num_(0.0), c.v.nan_to_num_(0.0)
+    m = torch.linalg.qr(torch.randn((h_kv, 128, 32), generator=torch.Generator().manual_seed(2)))[0]
+    layer = J.PagedLayer(c.k, c.v, c.bt, c.seq_lens, m.transpose(1, 2).contiguous().cuda(), 64,
+                         track_mass=True)
+    layer.prefill_scores()
+    q, kn, vn = (x.cuda() for x in (c.normal(2, n, h_kv * g, 128), c.normal(2, n, h_kv, 128),
+                                    c.normal(2, n, h_kv, 128)))
+    par = cuda([random_tree(c.rng, n) for _ in range(2)])
+    path, n_path = cuda([[0, 1], [0, 3]]), cuda([2, 1])
+    k1, v1 = kn[:, 0].contiguous(), vn[:, 0].contiguous()
+    q1 = q[:, 0].contiguous()
+    state = [c.k, c.v, layer.score_cache, layer.mass, layer.seq_lens]
+
+    def once():
+        a = layer.draft(q, kn, vn, par, sparse=True)
+        layer.commit(path, n_path)
+        layer.seq_lens += 1
+        b = layer.step(q1, k1, v1)[0].clone()
+        idx, count = layer.evict(60, 8)
+        return [a, b, idx, count]
+
+    start = [t.clone() for t in state]
+    want = [t.clone() for t in once()] + [t.clone() for t in state]
+
+    def reset():
+        for t, s in zip(state, start):
+            t.copy_(s)
+
+    reset()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        once()  # (workspaces of the layer)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = once()
+    for _ in range(2):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, outs + state))
+
+
+def test_draft_refuses_too_many_nodes():
+    J = jssa()
+    c = Paged([40], 80, 1, 128, seed=41)
+    layer = J.PagedLayer(c.k, c.v, c.bt, c.seq_lens, torch.zeros((1, 32, 128), device="cuda"), 16)
+    codes = layer.score_cache.clone()
+    kn = c.normal(1, 65, 1, 128).cuda()
+    with pytest.raises(ValueError):
+        layer.draft(c.normal(1, 65, 4, 128).cuda(), kn, kn, cuda([list(range(-1, 64))]))
+    assert torch.equal(layer.score_cache, codes)
+    with pytest.raises(ValueError):
+        layer.evict(8)

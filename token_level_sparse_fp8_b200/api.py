@@ -183,6 +183,11 @@ def _mass(t: torch.Tensor, name: str, batch: int, h_kv: int, capacity: int, like
     return p, row
 
 
+def _same_device(like: torch.Tensor, *tensors):
+    if any(t.get_device() != like.get_device() for t in tensors):
+        raise ValueError(f"every tensor of the call must be on {like.device}")
+
+
 def _codes(score_cache: Optional[torch.Tensor], num_pages, h_kv, page_size, like: torch.Tensor):
     """(pointer, bytes of a scoring row) of a scoring cache; (None, 0) without one."""
     if score_cache is None:
@@ -459,6 +464,7 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if mass is not None:
         bt, max_pages = _table(block_table, "block_table", batch, q)
         m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
+        _same_device(q, k_cache, v_cache)
         i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
         c = _arg(count, "count", torch.int32, (batch, h_kv), q)
         o = _arg(out, "out", torch.bfloat16, q.shape, q)
@@ -614,6 +620,7 @@ def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if mass is not None:
         bt, max_pages = _table(block_table, "block_table", batch, q)
         m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
+        _same_device(q, k_cache, v_cache)
         lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
         o = _arg(out, "out", torch.bfloat16, q.shape, q)
         p, n, _hold = _scratch(ws, _ws_bytes(FN_DENSE_DECODE_MASS, batch, h_q, h_kv, d, max_pages,
@@ -664,6 +671,7 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
     if mass is not None:
         bt, max_pages = _table(block_table, "block_table", batch, q)
         m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
+        _same_device(q, k_cache, v_cache, score_cache, basis)
         lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
         i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
         c = _arg(count, "count", torch.int32, (batch, h_kv), q)
@@ -876,6 +884,8 @@ class PagedLayer:
         ``seq_lens[b] + i``. ``sparse``: the context is the top-B selection of the mean query of
         the tree's used nodes, one set per KV head for the whole tree."""
         batch, n, h_kv, d = k_new.shape
+        if n > TREE_MAX_NODES:
+            raise ValueError(f"a tree has at most {TREE_MAX_NODES} nodes")
         slots = self._node_slots(parents)
         store(k_new.view(batch * n, h_kv, d), slots.view(-1), self.basis, self.score_cache)
         idx = count = None
@@ -884,7 +894,7 @@ class PagedLayer:
             mean = (torch.einsum("bnhd,bn->bhd", q.float(), used)
                     / used.sum(1).clamp(min=1.0)[:, None, None]).to(torch.bfloat16)
             idx, count = score_topk(mean, self.basis, self.score_cache, self.block_table,
-                                    self.seq_lens, self.budget, self.idx, self.count)
+                                    self.seq_lens, self.budget, self.idx, self.count, self.ws)
         return tree_attend(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens, parents,
                            k_new, v_new, idx, count, self.scale, window, out, self.ws_tree)
 
