@@ -118,8 +118,9 @@ __device__ __forceinline__ Tree tree_of(const TreeArgs& a, int b, int lane, bool
     bad[u] = p < -1 || p >= i;
     ptr[u] = bad[u] ? -1 : p;
   }
+  // (a tree of depth d takes log2 d rounds)
 #pragma unroll 1
-  for (int step = 1; step < a.n; step <<= 1) {
+  while (__any_sync(kAll, ptr[0] >= 0 || ptr[1] >= 0)) {
     uint64_t s[2];
     int np[2];
     bool nb[2];
