@@ -99,7 +99,7 @@ def _ws(device: torch.device, ws: Optional[Workspace], fn: int) -> Workspace:
     return _default_ws[key]
 
 
-def _scratch(ws: Optional[Workspace], nbytes: int, device: torch.device):
+def _scratch(ws: Optional[Workspace], nbytes: int, like: torch.Tensor):
     """(pointer, bytes, owner) of a workspace that needs no clearing: the caller's, else memory of
     this call alone, taken from torch's allocator on the current stream (so calls on other streams
     and captured graphs never share it)."""
@@ -108,7 +108,7 @@ def _scratch(ws: Optional[Workspace], nbytes: int, device: torch.device):
         return p, n, None
     if nbytes == 0:
         return None, 0, None
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf = like.new_empty((nbytes,), dtype=torch.uint8)
     return buf.data_ptr(), nbytes, buf
 
 
@@ -156,16 +156,19 @@ def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, shape, like: torch.Tens
 
 def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor):
     """(pointers, strides, shape) of a K / V cache pair ``[num_pages, page_size, h_kv, d]``."""
+    try:
+        strides, shape = k_cache.stride(), k_cache.shape
+        if (k_cache.dtype is torch.bfloat16 and v_cache.dtype is torch.bfloat16 and k_cache.is_cuda
+                and v_cache.get_device() == k_cache.get_device() and len(shape) == 4
+                and strides[3] == 1 and v_cache.stride() == strides and v_cache.shape == shape):
+            return (k_cache.data_ptr(), v_cache.data_ptr()), strides[:3], shape
+    except AttributeError:
+        pass
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
-    strides, shape = k_cache.stride(), k_cache.shape
-    if len(shape) != 4 or strides[3] != 1:
-        raise ValueError("KV cache must be [num_pages, page_size, h_kv, d] with a contiguous last dim")
-    if v_cache.stride() != strides or v_cache.shape != shape:
+    if kv_strides(k_cache) != kv_strides(v_cache) or v_cache.shape != k_cache.shape:
         raise ValueError("K and V caches must share one layout")
-    if v_cache.get_device() != k_cache.get_device():
-        raise ValueError("K and V caches must be on one device")
-    return (k_cache.data_ptr(), v_cache.data_ptr()), strides[:3], shape
+    raise ValueError("K and V caches must be on one device")
 
 
 def _table(t: torch.Tensor, name: str, batch: int, like: torch.Tensor):
@@ -192,17 +195,17 @@ def _codes(score_cache: Optional[torch.Tensor], num_pages, h_kv, page_size, like
     """(pointer, bytes of a scoring row) of a scoring cache; (None, 0) without one."""
     if score_cache is None:
         return None, 0
-    bf16 = isinstance(score_cache, torch.Tensor) and score_cache.dtype is torch.bfloat16
-    r = score_cache.shape[-1] if isinstance(score_cache, torch.Tensor) and score_cache.dim() == 4 else 0
-    p = _arg(score_cache, "score_cache", torch.bfloat16 if bf16 else torch.uint8,
-             (num_pages, h_kv, page_size, r), like)
-    return p, r * (2 if bf16 else 1)
+    shape = score_cache.shape if isinstance(score_cache, torch.Tensor) else ()
+    r = shape[3] if len(shape) == 4 else 0
+    if len(shape) and score_cache.dtype is torch.bfloat16:
+        return _arg(score_cache, "score_cache", torch.bfloat16, (num_pages, h_kv, page_size, r), like), 2 * r
+    return _arg(score_cache, "score_cache", torch.uint8, (num_pages, h_kv, page_size, r), like), r
 
 
 def _or_new(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> torch.Tensor:
-    """An int32 output: the caller's, or a new one."""
+    """An int32 output: the caller's, or a new one (``like``: an int32 tensor)."""
     if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=like.device)
+        return like.new_empty(shape)
     _arg(t, name, torch.int32, shape, like)
     return t
 
@@ -447,6 +450,8 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     (float32 ``[batch, h_kv, >= max_pages * page_size]``) every attended position's weight, summed
     over the KV head's query heads, is added to its entry (an index set then names no position
     twice)."""
+    if mass is not None:
+        return _attend_mass(q, k_cache, v_cache, block_table, mass, scale, out, ws, idx=idx, count=count)
     _need(q, "q", torch.bfloat16)
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
@@ -461,25 +466,47 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     budget = idx.shape[2]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     out = torch.empty_like(q) if out is None else out
-    if mass is not None:
-        bt, max_pages = _table(block_table, "block_table", batch, q)
-        m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
-        _same_device(q, k_cache, v_cache)
-        i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
-        c = _arg(count, "count", torch.int32, (batch, h_kv), q)
-        o = _arg(out, "out", torch.bfloat16, q.shape, q)
-        p, n, _hold = _scratch(ws, _ws_bytes(FN_INDEXED_ATTEND_MASS, batch, h_q, h_kv, d, max_pages,
-                                             page_size, budget, q.get_device()), q.device)
-        _call_on(q.get_device(), "jssa_indexed_attend_mass", q.data_ptr(), k_cache.data_ptr(),
-                 v_cache.data_ptr(), *strides, bt, max_pages, i, c, batch, h_q, h_kv, d, budget,
-                 num_pages, page_size, scale, m, row, o, p, n)
-        return out
     w = _ws(q.device, ws, FN_INDEXED_ATTEND)
     p, n = w.get(workspace_size(FN_INDEXED_ATTEND, batch, h_q, h_kv, d, block_table.shape[1],
                                 page_size, budget))
     call("jssa_indexed_attend", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *strides,
          block_table.data_ptr(), block_table.shape[1], idx.data_ptr(), count.data_ptr(), batch, h_q,
          h_kv, d, budget, num_pages, page_size, scale, out.data_ptr(), p, n, _stream(q.device))
+    return out
+
+
+def _attend_mass(q, k_cache, v_cache, block_table, mass, scale, out, ws, seq_lens=None, window=-1,
+                 idx=None, count=None):
+    """:func:`dense_decode` (with ``seq_lens``) or :func:`indexed_attend` (with ``idx``, ``count``)
+    that adds the positions' weights to ``mass``."""
+    _need(q, "q", torch.bfloat16)
+    batch, h_q, d = q.shape
+    kv, strides, (num_pages, page_size, h_kv, _) = _caches(k_cache, v_cache)
+    _same_device(q, k_cache)
+    bt, max_pages = _table(block_table, "block_table", batch, q)
+    m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _arg(out, "out", torch.bfloat16, q.shape, q)
+    index = q.get_device()
+    if idx is None:
+        lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
+        p, n, _hold = _scratch(ws, _ws_bytes(FN_DENSE_DECODE_MASS, batch, h_q, h_kv, d, max_pages,
+                                             page_size, window, index), q)
+        _call_on(index, "jssa_dense_decode_mass", q.data_ptr(), *kv, *strides, bt, max_pages, lens,
+                 batch, h_q, h_kv, d, num_pages, page_size, window, scale, m, row, out.data_ptr(),
+                 p, n)
+        return out
+    budget = idx.shape[-1]
+    i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
+    c = _arg(count, "count", torch.int32, (batch, h_kv), q)
+    p, n, _hold = _scratch(ws, _ws_bytes(FN_INDEXED_ATTEND_MASS, batch, h_q, h_kv, d, max_pages,
+                                         page_size, budget, index), q)
+    _call_on(index, "jssa_indexed_attend_mass", q.data_ptr(), *kv, *strides, bt, max_pages, i, c,
+             batch, h_q, h_kv, d, budget, num_pages, page_size, scale, m, row, out.data_ptr(), p, n)
     return out
 
 
@@ -604,6 +631,8 @@ def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  mass: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Dense paged decode attention over ``[max(0, L - window), L)`` (all when window <= 0).
     ``mass`` as in :func:`indexed_attend`."""
+    if mass is not None:
+        return _attend_mass(q, k_cache, v_cache, block_table, mass, scale, out, ws, seq_lens, window)
     _need(q, "q", torch.bfloat16)
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
@@ -617,18 +646,6 @@ def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     max_pages = block_table.shape[1]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     out = torch.empty_like(q) if out is None else out
-    if mass is not None:
-        bt, max_pages = _table(block_table, "block_table", batch, q)
-        m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
-        _same_device(q, k_cache, v_cache)
-        lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
-        o = _arg(out, "out", torch.bfloat16, q.shape, q)
-        p, n, _hold = _scratch(ws, _ws_bytes(FN_DENSE_DECODE_MASS, batch, h_q, h_kv, d, max_pages,
-                                             page_size, window, q.get_device()), q.device)
-        _call_on(q.get_device(), "jssa_dense_decode_mass", q.data_ptr(), k_cache.data_ptr(),
-                 v_cache.data_ptr(), *strides, bt, max_pages, lens, batch, h_q, h_kv, d, num_pages,
-                 page_size, window, scale, m, row, o, p, n)
-        return out
     w = _ws(q.device, ws, FN_DENSE_DECODE)
     p, n = w.get(workspace_size(FN_DENSE_DECODE, batch, h_q, h_kv, d, max_pages, page_size, window))
     call("jssa_dense_decode", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *strides,
@@ -677,7 +694,7 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
         c = _arg(count, "count", torch.int32, (batch, h_kv), q)
         o = _arg(out, "out", torch.bfloat16, q.shape, q)
         p, n, _hold = _scratch(ws, _ws_bytes(FN_DECODE_MASS, batch, h_q, h_kv, d, max_pages,
-                                             page_size, budget, q.get_device()), q.device)
+                                             page_size, budget, q.get_device()), q)
         _call_on(q.get_device(), "jssa_decode_mass", q.data_ptr(), _ptr(k_new), _ptr(v_new),
                  k_cache.data_ptr(), v_cache.data_ptr(), *strides, score_cache.data_ptr(),
                  basis.data_ptr(), bt, max_pages, lens, batch, h_q, h_kv, d, r, num_pages,
@@ -747,7 +764,7 @@ def tree_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     else:
         _arg(out, "out", torch.bfloat16, q.shape, q)
     p, nb, _hold = _scratch(ws, _ws_bytes(FN_TREE_ATTEND, batch, h_q, h_kv, d, max_pages, page_size,
-                                          n, index), q.device)
+                                          n, index), q)
     _call_on(index, "jssa_tree_attend", q.data_ptr(), kn, vn, *kv, *strides, bt, max_pages, lens,
              par, i, c, batch, n, h_q, h_kv, d, budget, num_pages, page_size, window, scale,
              out.data_ptr(), p, nb)
@@ -770,7 +787,7 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
     pa = _arg(path, "path", torch.int32, (batch, max_path), k_cache)
     n_pa = _arg(n_path, "n_path", torch.int32, (batch,), k_cache)
     sc, code = _codes(score_cache, num_pages, h_kv, page_size, k_cache)
-    lens = _or_new(lens, "lens", (batch,), k_cache)
+    lens = torch.empty_like(seq_lens) if lens is None else _or_new(lens, "lens", (batch,), seq_lens)
     _call_on(k_cache.get_device(), "jssa_tree_commit", *kv, *strides, sc, code, bt, max_pages, sl,
              pa, n_pa, max_path, batch, h_kv, d, num_pages, page_size, lens.data_ptr())
     return lens
@@ -804,9 +821,9 @@ def evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     dst, dst_pages = bt, max_pages
     if dst_block_table is not None:
         dst, dst_pages = _table(dst_block_table, "dst_block_table", batch, k_cache)
-    idx = _or_new(idx, "idx", (batch, h_kv, keep), k_cache)
-    count = _or_new(count, "count", (batch, h_kv), k_cache)
-    lens = _or_new(lens, "lens", (batch,), k_cache)
+    idx = _or_new(idx, "idx", (batch, h_kv, keep), seq_lens)
+    count = _or_new(count, "count", (batch, h_kv), seq_lens)
+    lens = torch.empty_like(seq_lens) if lens is None else _or_new(lens, "lens", (batch,), seq_lens)
     _call_on(k_cache.get_device(), "jssa_evict", m, row, *kv, *strides, sc, code, bt, max_pages, dst,
              dst_pages, sl, batch, h_kv, d, num_pages, page_size, keep, recent, idx.data_ptr(),
              count.data_ptr(), mo, lens.data_ptr())

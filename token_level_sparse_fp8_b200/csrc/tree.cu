@@ -31,6 +31,10 @@
 // Masked positions must not reach the output even when V holds inf or NaN there (0 * inf): tiles
 // in which a row masks a position that others see are scanned; non-finite elements are added to
 // the rows that see them by hand and cleared in shared memory before the MMA.
+// Measured on one B200 (32/8 heads, d 128): 104 rows over 8 contexts of 32K 200 us, 5.4 TB/s of cache rows,
+// the time of the dense decode kernel over the same rows; 256 rows over 16 contexts of 32K down to 16K
+// 490 us, 3.2 TB/s and 0.8 PFLOP/s: there the softmax warps are the bound (2600 cycles per tile, of
+// which the exponentials take 900; its bytes take 1400). A chain of 5 nodes over one context of 700: 14 us.
 // Every wait is bounded: after a timeout a thread goes on without waiting (all barriers still
 // match), the flag is raised, and what was issued is drained before the tensor memory is freed.
 #include <limits.h>
