@@ -318,6 +318,9 @@ def _tree_ref64(q, k, v, bt, lens, parents, window, scale):
     (2, 3001, 50, 8, 1, 256, -1),     # four row tiles at head dim 256
     (4, 9000, 31, 4, 2, 128, 1024),
     (40, 700, 12, 4, 8, 128, -1),     # more (sequence, head) pairs than SMs
+    (300, 40, 4, 4, 4, 128, -1),      # many pairs of a single tile
+    (300, 50, 2, 2, 4, 256, -1),
+    (150, 90, 40, 4, 4, 128, 30),     # many short pairs of two tiles, 160 rows, windowed
 ])
 def test_tree_attend_long(batch, L, n, g, h_kv, d, window):
     J = jssa()

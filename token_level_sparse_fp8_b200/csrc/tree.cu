@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
         if (!fail) fail = __any_sync(kAll, !tc::mbar_wait(b, parity & 1u, limit));
       };
       const uint32_t ts = tmem + C::kS + g * kTT, tp = tmem + C::kP + g * (kTT / 2), to = tmem + C::kO + g * D;
-      uint32_t n_s = 0, n_p = 0, n_q = 0;  // S and P V issued, segments
+      uint32_t n_s = 0, n_p = 0, n_q = 0;  // S and P V issued, segments with a tile
       int64_t k0 = 0;
       while (k0 < todo && !fail) {
         const int tiles = pair_of(a, pair).tiles;
@@ -336,8 +336,9 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
             ++lap;
           }
         };
-        wait(smem_u32(&s_bar[kBars * (kHalves ? 0 : g) + kBarQ]), n_q);
-        ++n_q;
+        // Q is announced to a group's warp only in segments with a tile for it: those it cannot fall
+        // behind in (a warp two phases late could not tell them apart)
+        if (i_s < n) wait(bar(kBarQ), n_q++);
         if (i_s < n) issue_s();
         for (int i = kHalves ? g : 0; i < n && !fail; i += kStride) {
           if (i_s < n) issue_s();
@@ -603,6 +604,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
         if (q_tmem) tc::tmem_wait_st();
         else tc::fence_proxy_async_smem();
         arrive(kBarQ);
+        if (kHalves && t1 - t0 > 1 && lane == 0) tc::mbar_arrive(smem_u32(&s_bar[kBars + kBarQ]));
       }
       float m_ref = -INFINITY, l = 0.f;
       bool have_o = false;
