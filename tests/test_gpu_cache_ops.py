@@ -80,7 +80,7 @@ class Paged:
 def fp32_slack(q, k, d, scale):
     """X of the module's tolerances; ``k`` without NaN."""
     top = float(np.abs(q).sum(-1).max()) * float(np.nanmax(np.abs(np.where(np.isfinite(k), k, 0))))
-    return 2 * (d * 2.0 ** -23 * scale * top + 2.0 ** -20)
+    return 2 * (d * 2.0 ** -23 * abs(scale) * top + 2.0 ** -20)
 
 
 def check_out(out, ref, mag, slack):
@@ -948,3 +948,13 @@ def test_draft_refuses_too_many_nodes():
     assert torch.equal(layer.score_cache, codes)
     with pytest.raises(ValueError):
         layer.evict(8)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+@pytest.mark.parametrize("g", [5, 6, 7])
+def test_tree_attend_odd_groups_and_scales(g, scale, d):
+    # a zero scale (the mean of the visible values) and a negative one; group sizes that are no power of 2
+    c = Paged([150, 0, 63], 23, 2, d, seed=g)
+    run_tree(c, 23, g, [random_tree(c.rng, 23, b) for b in range(3)], scale=scale)
+    assert jssa().device_error() == 0
