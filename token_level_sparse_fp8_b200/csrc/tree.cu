@@ -19,22 +19,26 @@
 //     S = Q K^T and the MN-major operand of O += P V. They run ahead over pair boundaries. The
 //     nodes' rows come from k_new when given; another warp writes them to the cache.
 //   * Groups of 4 warps, one thread per query row (tensor-memory lane): S from tensor memory, online
-//     softmax in registers (fp32, lazy rescale of O), P as bf16 back to tensor memory as the A
-//     operand of P V. A further warp per group issues its MMAs; S of the next tile is computed while
-//     the softmax of this one runs. At d = 128 two groups: both halves of 256 rows (Q of the second one in shared
-//     memory: tensor memory is full), or, with at most 128 rows, the even and the odd tiles of the
-//     same rows, whose O are merged at the end through tensor memory (the two groups' warps share
-//     lanes). At d = 256 O takes 256 columns and one group remains.
-//   * P is rounded to bf16 (half a step, at most 2^-8 of a weight): the tensor cores take bf16 beside the
-//     bf16 V; the sum l is kept from the fp32 weights.
+//     softmax in registers (fp32, lazy rescale of O), P as two bf16 parts back to tensor memory as the A
+//     operands of P V. A further warp per group issues its MMAs; S of the next tile is computed while
+//     the softmax of this one runs. At d = 128 two groups: both halves of 256 rows, or, with at most
+//     128 rows, the even and the odd tiles of the same rows, whose O are merged at the end through
+//     tensor memory (the two groups' warps share lanes). Their S, P and O fill tensor memory, so Q is
+//     an operand in shared memory. At d = 256 O takes 256 columns, one group remains, and Q fits.
+//   * The tensor cores take bf16 beside the bf16 V, so P = h + l (split_weights): a weight is off by at
+//     most 2^-14 of itself, as close as the decode kernels' split. The sum of the weights is kept
+//     from the fp32 ones.
 //   * Pairs cut between CTAs leave fp32 (m, l, O) partials; a second kernel merges them.
 // Masked positions must not reach the output even when V holds inf or NaN there (0 * inf): tiles
 // in which a row masks a position that others see are scanned; non-finite elements are added to
 // the rows that see them by hand and cleared in shared memory before the MMA.
-// Measured on one B200 (32/8 heads, d 128): 104 rows over 8 contexts of 32K 200 us, 5.4 TB/s of cache rows,
-// the time of the dense decode kernel over the same rows; 256 rows over 16 contexts of 32K down to 16K
-// 490 us, 3.2 TB/s and 0.8 PFLOP/s: there the softmax warps are the bound (2600 cycles per tile, of
-// which the exponentials take 900; its bytes take 1400). A chain of 5 nodes over one context of 700: 14 us.
+// Measured on one B200 (32/8 heads, d 128; replayed in a graph): 104 rows over 8 contexts of 32K down to
+// 16K 183 us, 4.2 TB/s of cache rows (the dense decode kernel: 156 us for one query each); 256 rows over
+// 16 such contexts 588 us, 2.7 TB/s and 0.67 PFLOP/s: there the softmax warps are the bound (2900 cycles
+// per tile, of which the exponentials and the split of P take 1400; the tensor pipe needs 1800, the bytes
+// 1400). With P as one bf16 the two took 490 and 154 us: the split adds instructions to the softmax, the
+// second product to the tensor pipe, and a stage is held longer. A chain of 5 nodes over one
+// context of 700: 16 us.
 // Every wait is bounded: after a timeout a thread goes on without waiting (all barriers still
 // match), the flag is raised, and what was issued is drained before the tensor memory is freed.
 #include <limits.h>
@@ -75,12 +79,17 @@ struct Cfg {
   static constexpr int kBlockBytes = kTT * 128;              // 64 tokens x 64 dimensions
   static constexpr int kTileBytes = D / 64 * kBlockBytes;    // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kTileBytes;         // K then V
-  static constexpr int kQBytes = TWO ? kM * D * 2 : 0;       // Q of group 1
-  static constexpr int kStages = D == 128 ? (TWO ? 5 : 6) : 3;
+  // Q: in shared memory at d = 128 (of both groups, or of the rows they share), in tensor memory at
+  // d = 256
+  static constexpr bool kQTmem = D != 128;
+  static constexpr int kQGroup = kM * D * 2;
+  static constexpr int kQBytes = kQTmem ? 0 : (TWO ? 2 : 1) * kQGroup;
+  static constexpr int kStages = D == 128 ? (TWO ? 4 : 5) : 3;
   static constexpr int kSmem = 1024 + kQBytes + kStages * kStageBytes;
-  // tensor memory columns: Q (A operand, bf16) of group 0 (of both), P of each group (A operand,
-  // bf16), S and O of each group (fp32)
-  static constexpr uint32_t kQ = 0, kP = D == 128 ? 64 : 192, kS = 128, kO = 256;
+  // tensor memory columns: Q (d = 256) and P (high parts, then low parts) as bf16 A operands, S and O
+  // (fp32); P, S and O of each group
+  static constexpr int kPiece = D == 128 ? 8 : 32;  // pairs of weights written to P at a time
+  static constexpr uint32_t kQ = 0, kP = D == 128 ? 0 : 192, kS = 128, kO = 256;
 };
 
 // What the tiles of one (sequence, KV head) walk over: list index j < n_ctx is context position
@@ -152,6 +161,19 @@ __device__ __forceinline__ Tree tree_of(const TreeArgs& a, int b, int lane, bool
     if (bad[u]) t.see[u] = 0ull;
   }
   return t;
+}
+
+// Two weights p = h + l as pairs of bf16 (the first one in the low half): h is p cut off, l the rest,
+// with 2^-20 p added so that l > 0 wherever p > 0: an infinite value keeps its sign under both products
+// and never meets a zero weight that the formula does not have. l < 2^-7 p; its rounding (half a step)
+// and the addition are off by less than 2^-14 p.
+__device__ __forceinline__ void split_weights(float2 p, uint32_t& h, uint32_t& l) {
+  const uint32_t x = __float_as_uint(p.x), y = __float_as_uint(p.y);
+  h = __byte_perm(x, y, 0x7632);
+  const float2 minus_h = make_float2(__uint_as_float((x & 0xFFFF0000u) | 0x80000000u),
+                                     __uint_as_float((y & 0xFFFF0000u) | 0x80000000u));
+  const float2 rest = fma2(p, make_float2(1.f + 0x1p-20f, 1.f + 0x1p-20f), minus_h);
+  l = pack_bf16x2(rest.x, rest.y);
 }
 
 // Weight of a partial (m, l) under the merged maximum M; a row whose every score was NaN keeps it.
@@ -296,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
       auto wait = [&](uint32_t b, uint32_t parity) {  // (the whole warp agrees)
         if (!fail) fail = __any_sync(kAll, !tc::mbar_wait(b, parity & 1u, limit));
       };
-      const uint32_t ts = tmem + C::kS + g * kTT, tp = tmem + C::kP + g * (kTT / 2), to = tmem + C::kO + g * D;
+      const uint32_t ts = tmem + C::kS + g * kTT, tp = tmem + C::kP + g * kTT, to = tmem + C::kO + g * D;
       uint32_t n_s = 0, n_p = 0, n_q = 0;  // S and P V issued, segments with a tile
       int64_t k0 = 0;
       while (k0 < todo && !fail) {
@@ -313,8 +335,8 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
           tc::fence_proxy_async_smem();
           tc::fence_after_sync();
           const uint64_t b0 = tc::sw128_desc(ring + st_s * C::kStageBytes, 16, 1024);
-          const uint64_t a0 = tc::sw128_desc(q_smem, 16, 1024);
-          if (TWO && g == 1) {
+          const uint64_t a0 = tc::sw128_desc(q_smem + (TWO ? g * C::kQGroup : 0), 16, 1024);
+          if (!C::kQTmem) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               tc::mma_ss_warp(on, ts, a0 + (uint64_t)(((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4),
@@ -349,9 +371,9 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
                                              C::kBlockBytes, 1024);
           const bool add = *(volatile uint32_t*)&s_keep[g] != 0u;
 #pragma unroll
-          for (int kk = 0; kk < kTT / 16; ++kk)
-            tc::mma_ts_warp(on, to, tp + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
-                            add || kk > 0);
+          for (int kk = 0; kk < kTT / 8; ++kk)  // the high parts of P, then the low ones
+            tc::mma_ts_warp(on, to, tp + kk * 8, b0 + (uint64_t)((kk % (kTT / 16) * 16 * 128) >> 4),
+                            kIdescO, add || kk > 0);
           tc::mma_commit_warp(on, bar(kBarO));
           tc::mma_commit_warp(on, smem_u32(&s_empty[st_p]));
           ++n_p;
@@ -544,7 +566,8 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
     const int g = warp >> 2, gt = tid & (kM - 1);  // group, thread of the group = tensor-memory lane
     const int gbar = 1 + g;                        // the group's named barrier; 3: both groups
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
-    const uint32_t ts = tl + C::kS + g * kTT, tp = tl + C::kP + g * (kTT / 2), to = tl + C::kO + g * D;
+    const uint32_t ts = tl + C::kS + g * kTT, tp = tl + C::kP + g * kTT, to = tl + C::kO + g * D;
+    const uint32_t q_group = q_smem + (TWO ? g * C::kQGroup : 0);
     auto bar = [&](int which) { return smem_u32(&s_bar[kBars * g + which]); };
     // this warp has done its part: its tensor-memory accesses are complete before the arrival
     auto arrive = [&](int which) {
@@ -561,7 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
     int64_t k0 = 0;    // line index (within the CTA) of the segment's first tile
     while (k0 < todo) {
       // Q: this thread's row (on its way to L1 while the pair and the tree are resolved)
-      const bool q_tmem = !TWO || g == 0, q_mine = !kHalves || g == 0;
+      const bool q_mine = !kHalves || g == 0;
       const int pb = pair / a.h_kv;
       const int64_t q_off = r < rows ? (((int64_t)pb * a.n + node) * a.h_q + (int64_t)(pair - pb * a.h_kv) * G + r % G) * D : 0;
       const uint4* qrow = reinterpret_cast<const uint4*>(a.q + q_off);
@@ -592,16 +615,16 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
             v[4 * u + 2] = used ? x.z ^ flip : 0u;
             v[4 * u + 3] = used ? x.w ^ flip : 0u;
           }
-          if (q_tmem) {
+          if (C::kQTmem) {
             tc::tmem_st32(tl + C::kQ + 32 * c, v);
           } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              st_shared_v4(q_smem + c * kM * 128 + gt * 128 + ((u ^ (gt & 7)) << 4), v[4 * u],
+              st_shared_v4(q_group + c * kM * 128 + gt * 128 + ((u ^ (gt & 7)) << 4), v[4 * u],
                            v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
           }
         }
-        if (q_tmem) tc::tmem_wait_st();
+        if (C::kQTmem) tc::tmem_wait_st();
         else tc::fence_proxy_async_smem();
         arrive(kBarQ);
         if (kHalves && t1 - t0 > 1 && lane == 0) tc::mbar_arrive(smem_u32(&s_bar[kBars + kBarQ]));
@@ -689,22 +712,32 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
           const float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
           const float2 sc2 = make_float2(scale_log2, scale_log2), ms2 = make_float2(-m_sub, -m_sub);
           float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-          uint32_t ph[32];
+          // kPiece pairs at a time, so that P takes the registers that S gives up (d = 256 has registers for the
+          // whole tile, and the previous P V is later)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float2 p = j < 16 ? make_float2(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1]))
-                              : make_float2(__uint_as_float(s1[2 * j - 32]), __uint_as_float(s1[2 * j - 31]));
-            p = fma2(p, sc2, ms2);
-            p.x = fast_exp2(p.x);
-            p.y = fast_exp2(p.y);
-            if (j & 1) sum1 = add2(sum1, p);
-            else sum0 = add2(sum0, p);
-            ph[j] = pack_bf16x2(p.x, p.y);
+          for (int j0 = 0; j0 < 32; j0 += C::kPiece) {
+            uint32_t ph[C::kPiece], pl[C::kPiece];
+#pragma unroll
+            for (int u = 0; u < C::kPiece; ++u) {
+              const int j = j0 + u;
+              float2 p = j < 16 ? make_float2(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1]))
+                                : make_float2(__uint_as_float(s1[2 * j - 32]), __uint_as_float(s1[2 * j - 31]));
+              p = fma2(p, sc2, ms2);
+              p.x = fast_exp2(p.x);
+              p.y = fast_exp2(p.y);
+              if (j & 1) sum1 = add2(sum1, p);
+              else sum0 = add2(sum0, p);
+              split_weights(p, ph[u], pl[u]);
+            }
+            if (j0 == 0) previous_done();
+#pragma unroll
+            for (int u = 0; u < C::kPiece; u += 8) {
+              tc::tmem_st8(tp + j0 + u, ph + u);
+              tc::tmem_st8(tp + kTT / 2 + j0 + u, pl + u);
+            }
           }
           sum0 = add2(sum0, sum1);
           l = l * corr + (sum0.x + sum0.y);
-          previous_done();
-          tc::tmem_st32(tp, ph);
           tc::tmem_wait_st();
         } else {
           // (keeps this warp's arrivals in step: P of the previous tile has been taken)
@@ -732,9 +765,10 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
             const unsigned two = __ballot_sync(kAll, mine);
             if (lane == 0) s_bad[g][warp & 3] = two;  // bit 2 i (+ 1): token 16 w + i
             tc::bar_sync(gbar, kM);
-            // add p v of the non-finite elements to the rows that see them (O = 0 first)
-            uint32_t pl[32];
-            tc::tmem_ld32(tp, pl);
+            // add p v of the non-finite elements to the rows that see them (O = 0 first; the high part
+            // of p has its sign, and is 0 or NaN where p is)
+            uint32_t pw[32];
+            tc::tmem_ld32(tp, pw);
             tc::tmem_wait_ld();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -749,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
 #pragma unroll 1
               for (int j = 0; j < kTT; ++j) {
                 if (!((s_bad[g][j >> 4] >> (2 * (j & 15))) & 3u)) continue;
-                const uint32_t w = pl[j >> 1];
+                const uint32_t w = pw[j >> 1];
                 const float pj = (j & 1) ? bf16_hi(w) : bf16_lo(w);
                 const bool sees = (see_t >> j) & 1ull;
 #pragma unroll
