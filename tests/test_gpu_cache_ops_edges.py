@@ -68,3 +68,64 @@ def test_tree_attend_visible_infinities(n, d):
     assert bool((out[..., 5] == math.inf).all()) and bool((out[..., 7] == -math.inf).all())
     out[..., 5] = out[..., 7] = 0.0
     assert bool(torch.isfinite(out).all())
+
+
+# ------------------------------------------------------------------------------------------------
+# the layer
+# ------------------------------------------------------------------------------------------------
+
+
+def make_layer(lens, h_kv=2, d=128, r=32, budget=64, extra=80, seed=70, track_mass=True):
+    J = jssa()
+    c = Paged(lens, extra, h_kv, d, seed=seed)
+    c.k.nan_to_num_(0.0), c.v.nan_to_num_(0.0)
+    m = torch.linalg.qr(torch.randn((h_kv, d, r), generator=torch.Generator().manual_seed(seed)))[0]
+    layer = J.PagedLayer(c.k, c.v, c.bt, c.seq_lens, m.transpose(1, 2).contiguous().cuda(), budget,
+                         track_mass=track_mass)
+    layer.prefill_scores()
+    return c, layer
+
+
+def test_captured_calls_of_every_size_keep_their_memory():
+    # graphs of calls whose workspaces grow from one to the next; what is allocated afterwards must not
+    # share memory with any of them
+    c, layer = make_layer([900, 333], extra=80)
+    g, nodes = 4, (8, 64)
+    q = {n: c.normal(2, n, 2 * g, 128).cuda() for n in nodes}
+    kn, vn = ({n: c.normal(2, n, 2, 128).cuda() for n in nodes} for _ in range(2))
+    par = {n: cuda([random_tree(c.rng, n) for _ in range(2)]) for n in nodes}
+    q1 = q[8][:, 0].contiguous()
+    calls = [lambda: layer.step(q1)[0].clone(), lambda: layer.dense(q1, window=64),
+             lambda: layer.dense(q1)]
+    for n in nodes:
+        for sparse in (False, True):
+            calls.append(lambda n=n, sparse=sparse: layer.draft(q[n], kn[n], vn[n], par[n], sparse=sparse))
+    k0, v0, codes = c.k.clone(), c.v.clone(), layer.score_cache.clone()
+
+    def reset():
+        c.k.copy_(k0), c.v.copy_(v0), layer.score_cache.copy_(codes), layer.mass.zero_()
+
+    want = []
+    for f in calls:
+        reset()
+        want.append((f().clone(), layer.mass.clone()))
+    graphs, outs = [], []
+    for f in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(f())
+        graphs.append(graph)
+    for f in calls:
+        reset()
+        f()
+    torch.cuda.synchronize()
+    patterns = [torch.full((1 << k,), 90 + k, dtype=torch.uint8, device="cuda")
+                for k in range(12, 25) for _ in range(3)]
+    for graph, out, (ref, mass) in zip(graphs, outs, want):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(layer.mass, mass)
+    for i, p in enumerate(patterns):
+        assert bool((p == 90 + 12 + i // 3).all())
+    assert jssa().device_error() & ~16 == 0

@@ -54,6 +54,10 @@ def default_rank(head_dim: int) -> int:
     return head_dim // 4
 
 
+def _capturing() -> bool:
+    return torch.cuda.is_current_stream_capturing()
+
+
 def kv_strides(cache: torch.Tensor) -> Tuple[int, int, int]:
     """(page, slot, head) element strides of a ``[num_pages, page_size, h_kv, d]`` cache view."""
     if cache.dim() != 4 or cache.stride(3) != 1:
@@ -70,11 +74,14 @@ def workspace_size(fn: int, batch: int, h_q: int, h_kv: int, d: int, max_pages: 
 
 
 class Workspace:
-    """A zero-initialised device workspace that grows on demand (one per stream of use)."""
+    """A zero-initialised device workspace that grows on demand (one per stream of use). A buffer
+    that a captured graph was given lives as long as the workspace does, also after a larger call
+    has replaced it."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self._captured = []  # buffers given out while a graph was being captured
 
     def get(self, nbytes: int) -> Tuple[Optional[int], int]:
         if nbytes == 0:
@@ -82,7 +89,21 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             call("jssa_workspace_init", self.buf.data_ptr(), self.buf.numel(), _stream(self.device))
+        if _capturing() and not any(b is self.buf for b in self._captured):
+            self._captured.append(self.buf)
         return self.buf.data_ptr(), self.buf.numel()
+
+
+class _CallWorkspace:
+    """Workspace of one call of an entry point that needs no clearing: memory from torch's allocator
+    on the current stream, so calls on other streams and captured graphs share nothing."""
+
+    def __init__(self, device):
+        self.device, self.buf = device, None
+
+    def get(self, nbytes: int) -> Tuple[Optional[int], int]:
+        self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        return self.buf.data_ptr(), nbytes
 
 
 _default_ws = {}
@@ -872,8 +893,8 @@ class PagedLayer:
         # running attention mass of every position (what `evict` goes by); None: not kept
         self.mass = (torch.zeros((batch, h_kv, block_table.shape[1] * page_size),
                                  dtype=torch.float32, device=k_cache.device) if track_mass else None)
-        self.ws_mass = Workspace(k_cache.device)   # steps that keep the mass
-        self.ws_tree = Workspace(k_cache.device)   # drafted trees
+        # (steps that keep the mass and drafted trees come in several sizes: their workspaces are
+        # taken by each call)
 
     def prefill_scores(self, chunk_pages: int = 4096) -> None:
         """Store the scoring code of every cached position (all slots of every page)."""
@@ -888,12 +909,12 @@ class PagedLayer:
     def step(self, q, k_new=None, v_new=None, out=None):
         return decode(q, k_new, v_new, self.k_cache, self.v_cache, self.score_cache, self.basis,
                       self.block_table, self.seq_lens, self.budget, self.scale, out, self.idx,
-                      self.count, self.ws if self.mass is None else self.ws_mass, self.mass)
+                      self.count, self.ws if self.mass is None else None, self.mass)
 
     def dense(self, q, out=None, window=-1):
         return dense_decode(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens,
                             self.scale, window, out,
-                            self.ws_dense if self.mass is None else self.ws_mass, self.mass)
+                            self.ws_dense if self.mass is None else None, self.mass)
 
     def draft(self, q, k_new, v_new, parents, out=None, window=-1, sparse=False):
         """Attention of a tree of drafted tokens that follow the ``seq_lens`` committed ones
@@ -911,9 +932,10 @@ class PagedLayer:
             mean = (torch.einsum("bnhd,bn->bhd", q.float(), used)
                     / used.sum(1).clamp(min=1.0)[:, None, None]).to(torch.bfloat16)
             idx, count = score_topk(mean, self.basis, self.score_cache, self.block_table,
-                                    self.seq_lens, self.budget, self.idx, self.count, self.ws)
+                                    self.seq_lens, self.budget, self.idx, self.count,
+                                    _CallWorkspace(q.device))
         return tree_attend(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens, parents,
-                           k_new, v_new, idx, count, self.scale, window, out, self.ws_tree)
+                           k_new, v_new, idx, count, self.scale, window, out)
 
     def _node_slots(self, parents):
         """Flat cache slots of the tree's nodes (int64 ``[batch, n]``; -1 where a node is unused
