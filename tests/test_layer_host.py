@@ -31,3 +31,54 @@ def test_workspace_keeps_what_a_captured_graph_holds(cpu_workspace):
     ws.get(9000)
     assert dropped() is None  # no graph was given that one
     assert held() is not None
+
+
+def _decode_args(d=128, h_kv=2, r=32, batch=2):
+    """Arguments of a decode step on host memory: (q, k_new, v_new, k, v, codes, basis, table, lens)."""
+    bf = torch.bfloat16
+    k = torch.zeros((6, 16, h_kv, d), dtype=bf)
+    return dict(q=torch.zeros((batch, 4 * h_kv, d), dtype=bf), k_new=torch.zeros((batch, h_kv, d), dtype=bf),
+                v_new=torch.zeros((batch, h_kv, d), dtype=bf), k_cache=k, v_cache=k.clone(),
+                score_cache=torch.zeros((6, h_kv, 16, r), dtype=torch.uint8),
+                basis=torch.zeros((h_kv, r, d)), block_table=torch.zeros((batch, 3), dtype=torch.int32),
+                seq_lens=torch.ones((batch,), dtype=torch.int32))
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """Arguments may be on the host; a call that gets as far as the library fails the test."""
+    def launched(*a, **k):
+        raise AssertionError("the call was not refused")
+
+    monkeypatch.setattr(api, "_need", lambda *a, **k: None)
+    for name in ("call", "_call_on", "_ws", "_scratch", "_caches", "_table", "_arg", "_same_device"):
+        monkeypatch.setattr(api, name, launched)
+
+
+@pytest.mark.parametrize("with_mass", [False, True])
+@pytest.mark.parametrize("q_dim,cache_dim", [(256, 128), (128, 256)])
+def test_attention_refuses_another_head_dim(no_launch, q_dim, cache_dim, with_mass):
+    # rows of another length would be read past their ends
+    a = _decode_args(cache_dim)
+    q = torch.zeros((2, 8, q_dim), dtype=torch.bfloat16)
+    mass = torch.zeros((2, 2, 48)) if with_mass else None
+    idx, count = torch.zeros((2, 2, 8), dtype=torch.int32), torch.ones((2, 2), dtype=torch.int32)
+    with pytest.raises(ValueError, match="head dim"):
+        api.dense_decode(q, a["k_cache"], a["v_cache"], a["block_table"], a["seq_lens"], mass=mass)
+    with pytest.raises(ValueError, match="head dim"):
+        api.indexed_attend(q, a["k_cache"], a["v_cache"], a["block_table"], idx, count, mass=mass)
+    with pytest.raises(ValueError, match="head dim"):
+        api.decode(**{**a, "q": q}, budget=8, mass=mass)
+
+
+@pytest.mark.parametrize("with_mass", [False, True])
+@pytest.mark.parametrize("name,shape", [
+    ("v_cache", (5, 16, 2, 128)), ("score_cache", (5, 2, 16, 32)), ("score_cache", (6, 2, 8, 32)),
+    ("score_cache", (6, 2, 16, 16)), ("basis", (1, 32, 128)), ("basis", (2, 32, 64)),
+    ("k_new", (1, 2, 128)), ("v_new", (2, 1, 128)),
+])
+def test_decode_refuses_other_shapes(no_launch, name, shape, with_mass):
+    a = _decode_args()
+    a[name] = torch.zeros(shape, dtype=a[name].dtype)
+    with pytest.raises(ValueError, match="shape|agree"):
+        api.decode(**a, budget=8, mass=torch.zeros((2, 2, 48)) if with_mass else None)

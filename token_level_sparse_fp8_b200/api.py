@@ -207,6 +207,13 @@ def _mass(t: torch.Tensor, name: str, batch: int, h_kv: int, capacity: int, like
     return p, row
 
 
+def _head_dim(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor):
+    """The kernels read ``d`` elements of a cache row, ``d`` from the query: both caches must have it."""
+    if k_cache.shape[-1] != q.shape[-1] or v_cache.shape != k_cache.shape:
+        raise ValueError(f"the caches must agree with the head dim {q.shape[-1]} of q and with each "
+                         f"other, got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+
+
 def _same_device(like: torch.Tensor, *tensors):
     if any(t.get_device() != like.get_device() for t in tensors):
         raise ValueError(f"every tensor of the call must be on {like.device}")
@@ -480,6 +487,7 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     _need(idx, "idx", torch.int32)
     _need(count, "count", torch.int32)
     batch, h_q, d = q.shape
+    _head_dim(q, k_cache, v_cache)
     num_pages, page_size, h_kv, _ = k_cache.shape
     strides = kv_strides(k_cache)
     if kv_strides(v_cache) != strides:
@@ -502,6 +510,7 @@ def _attend_mass(q, k_cache, v_cache, block_table, mass, scale, out, ws, seq_len
     that adds the positions' weights to ``mass``."""
     _need(q, "q", torch.bfloat16)
     batch, h_q, d = q.shape
+    _head_dim(q, k_cache, v_cache)
     kv, strides, (num_pages, page_size, h_kv, _) = _caches(k_cache, v_cache)
     _same_device(q, k_cache)
     bt, max_pages = _table(block_table, "block_table", batch, q)
@@ -660,6 +669,7 @@ def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     _need(block_table, "block_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32)
     batch, h_q, d = q.shape
+    _head_dim(q, k_cache, v_cache)
     num_pages, page_size, h_kv, _ = k_cache.shape
     strides = kv_strides(k_cache)
     if kv_strides(v_cache) != strides:
@@ -695,8 +705,14 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
     batch, h_q, d = q.shape
+    _head_dim(q, k_cache, v_cache)
     num_pages, page_size, h_kv, _ = k_cache.shape
     r = basis.shape[1]
+    for t, n, shape in ((basis, "basis", (h_kv, r, d)),
+                        (score_cache, "score_cache", (num_pages, h_kv, page_size, r)),
+                        (k_new, "k_new", (batch, h_kv, d)), (v_new, "v_new", (batch, h_kv, d))):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
     strides = kv_strides(k_cache)
     if kv_strides(v_cache) != strides:
         raise ValueError("K and V caches must share one layout")
@@ -709,7 +725,7 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
     if mass is not None:
         bt, max_pages = _table(block_table, "block_table", batch, q)
         m, row = _mass(mass, "mass", batch, h_kv, max_pages * page_size, q)
-        _same_device(q, k_cache, v_cache, score_cache, basis)
+        _same_device(q, k_cache, v_cache, score_cache, basis, *(() if k_new is None else (k_new, v_new)))
         lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
         i = _arg(idx, "idx", torch.int32, (batch, h_kv, budget), q)
         c = _arg(count, "count", torch.int32, (batch, h_kv), q)
