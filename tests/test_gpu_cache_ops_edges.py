@@ -129,3 +129,25 @@ def test_captured_calls_of_every_size_keep_their_memory():
     for i, p in enumerate(patterns):
         assert bool((p == 90 + 12 + i // 3).all())
     assert jssa().device_error() & ~16 == 0
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_draft_with_lengths_outside_the_table(sparse):
+    # a negative length counts as 0, one past the table as the table's: flagged, and the layer lives on
+    J = jssa()
+    c, layer = make_layer([40, 25], extra=80, seed=71)
+    cap = c.table.shape[1] * 16
+    q, kn, vn = c.normal(2, 5, 8, 128), c.normal(2, 5, 2, 128), c.normal(2, 5, 2, 128)
+    par = [random_tree(c.rng, 5) for _ in range(2)]
+    want = None
+    for bad, as_if, flag in ((-40, 0, 4), (0, 0, 0), (10 ** 6, cap, 4 | 2), (cap, cap, 2)):
+        layer.seq_lens.copy_(cuda([bad, 25]))
+        out = layer.draft(q.cuda(), kn.cuda(), vn.cuda(), cuda(par), sparse=sparse)
+        assert J.device_error() & ~16 == flag
+        # the stored rows and codes, and the output, are those of the length it counts as
+        got = [out, c.k.clone(), c.v.clone(), layer.score_cache.clone()]
+        if bad != as_if:
+            want = got
+        else:
+            assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert layer.seq_lens.tolist() == [cap, 25]

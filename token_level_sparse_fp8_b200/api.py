@@ -958,7 +958,9 @@ class PagedLayer:
         or beyond the block table)."""
         n = parents.shape[1]
         max_pages = self.block_table.shape[1]
-        pos = self.seq_lens.long()[:, None] + torch.arange(n, device=parents.device)[None]
+        # (a negative length counts as 0, as in the library, which flags it)
+        pos = (self.seq_lens.long().clamp(min=0)[:, None]
+               + torch.arange(n, device=parents.device)[None])
         ok = (parents >= -1) & (pos < max_pages * self.page_size)
         page = torch.gather(self.block_table, 1,
                             (pos // self.page_size).clamp(max=max_pages - 1)).long()
