@@ -498,6 +498,21 @@ JSSA_API int jssa_tree_attend(const jssa_bf16* q, const jssa_bf16* k_new, const 
                               jssa_bf16* out, void* ws, size_t ws_bytes, jssa_stream_t stream);
 
 /*
+ * What a drafted tree needs around jssa_tree_attend, with the same nodes, lengths and pages:
+ *   slots[b, i] (int64 [batch, n_nodes], for jssa_store) = the flat slot of position seq_lens[b] + i
+ * for a used node, -1 for an unused one, past the end of the block table or on an unusable page;
+ *   q_mean[b] (bf16 [batch, h_q, d], for jssa_score_topk; NULL: not wanted, and q is not read) = the
+ * mean of the used nodes' queries, summed in fp32 and rounded once (zero without a used node): the query
+ * of one selection for the whole tree. Unused nodes' queries are not read. Lengths outside the table are
+ * clamped, bad parents make a node unused; both are flagged by jssa_tree_attend, not here. q as there,
+ * q_mean 16-byte aligned. No workspace.
+ */
+JSSA_API int jssa_tree_prepare(const jssa_bf16* q, const int32_t* parents, const int32_t* block_table,
+                               int max_pages, const int32_t* seq_lens, int batch, int n_nodes, int h_q,
+                               int d, int64_t num_pages, int page_size, int64_t* slots,
+                               jssa_bf16* q_mean, jssa_stream_t stream);
+
+/*
  * Commit of the accepted nodes of a drafted tree: for i < n_path[b] the row of position
  * seq_lens[b] + path[b, i] (K, V and, when score_cache is non-NULL, the scoring row) moves to
  * position seq_lens[b] + i, for every KV head; lens_out[b] = seq_lens[b] + n_path[b]. path int32

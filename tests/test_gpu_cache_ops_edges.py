@@ -151,3 +151,88 @@ def test_draft_with_lengths_outside_the_table(sparse):
         else:
             assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert layer.seq_lens.tolist() == [cap, 25]
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_draft_leaves_dropped_nodes_out(sparse):
+    # a node that names itself, a later or an unused one takes no part, nor do the nodes below it: no
+    # rows, no codes, no share in the query that selects the context
+    J = jssa()
+    c, layer = make_layer([300, 120], extra=80, seed=72)
+    par = [[-1, 0, 2, 5, 1, 4, -2, 6, 3, 0], [-1, -3, 1, 2, 0, 0, 9, 6, 7, 8]]
+    n = len(par[0])
+    q, kn, vn = c.normal(2, n, 8, 128), c.normal(2, n, 2, 128), c.normal(2, n, 2, 128)
+    used = [C.used_nodes(p) for p in par]
+    for b in range(2):  # (of the size that decides the selection, had they a share)
+        q[b, torch.as_tensor(~used[b])] *= 20
+    before = [c.k.clone(), c.v.clone(), layer.score_cache.clone()]
+    out = layer.draft(q.cuda(), kn.cuda(), vn.cuda(), cuda(par), sparse=sparse)
+    assert J.device_error() & ~16 == 2
+    for b, L in enumerate(c.lens):
+        for i in range(n):
+            page, slot = c.table[b, (L + i) // 16], (L + i) % 16
+            now = [c.k[page, slot], c.v[page, slot], layer.score_cache[page, :, slot]]
+            was = [before[0][page, slot], before[1][page, slot], before[2][page, :, slot]]
+            if used[b][i]:
+                assert torch.equal(now[0].cpu(), kn[b, i]) and not torch.equal(now[2], was[2])
+            else:
+                assert all(torch.equal(x, y) for x, y in zip(now, was))
+    idx = count = None
+    if sparse:
+        mean = torch.stack([q[b, torch.as_tensor(used[b])].double().mean(0) for b in range(2)])
+        idx, count = J.score_topk(mean.to(torch.bfloat16).cuda(), layer.basis, layer.score_cache, c.bt,
+                                  c.seq_lens, layer.budget)
+        same = (idx[..., None] == layer.idx[:, :, None]).any(-1).float().mean()
+        assert float(same) > 0.95  # (a mean rounded from float32 or float64 may differ by a bf16 step)
+        idx, count = layer.idx.cpu().numpy(), layer.count.cpu().numpy()
+    scale = 1 / math.sqrt(128)
+    ref, mag = C.tree_attend(f64(q), f64(c.k), f64(c.v), c.table, c.lens, par, scale, -1, idx, count)
+    check_close(f64(out), ref, mag, weight_slack(f64(q), f64(c.k), scale, 310))
+
+
+def test_draft_selects_without_the_padding():
+    # what an unused node's query holds reaches nothing
+    J = jssa()
+    c, layer = make_layer([500, 120], extra=80, seed=73)
+    par = cuda([[-1, 0, 0, -2, -7], [-1, -1, -5, -5, -5]])
+    q, kn, vn = c.normal(2, 5, 8, 128).cuda(), c.normal(2, 5, 2, 128).cuda(), c.normal(2, 5, 2, 128).cuda()
+    want = layer.draft(q, kn, vn, par, sparse=True).clone()
+    idx = layer.idx.clone()
+    for bad in (NAN, math.inf, 3e38):
+        q[0, 3:], q[1, 2:] = bad, bad
+        out = layer.draft(q, kn, vn, par, sparse=True)
+        assert torch.equal(layer.idx, idx) and torch.equal(out, want)
+    assert J.device_error() & ~16 == 0
+
+
+@pytest.mark.parametrize("d,r", [(128, 32), (256, 64)])
+@pytest.mark.parametrize("n", [0, 1, 33, 64])
+def test_draft_sizes(n, d, r):
+    # the slots and the mean query of trees of every width, no nodes among them
+    J = jssa()
+    c, layer = make_layer([77, 0, 200], h_kv=1, d=d, r=r, extra=80, seed=74)
+    par = [random_tree(c.rng, n, unused=min(n, b)) for b in range(3)]
+    q, kn, vn = c.normal(3, n, 3, d), c.normal(3, n, 1, d), c.normal(3, n, 1, d)
+    par = torch.as_tensor(np.asarray(par).reshape(3, n))
+    slots, mean = J.api._tree_prepare(q.cuda(), cuda(par), c.bt, c.seq_lens, c.k.shape[0], 16, True)
+    used = [C.used_nodes(par[b].tolist()) for b in range(3)]
+    for b, L in enumerate(c.lens):
+        pos = L + np.arange(n)
+        want = np.where(used[b], c.table[b][pos // 16] * 16 + pos % 16, -1) if n else np.zeros(0)
+        assert np.array_equal(slots.view(3, n)[b].cpu().numpy(), want)
+        rows = q[b, torch.as_tensor(used[b])].double()
+        ref = rows.mean(0).numpy() if len(rows) else np.zeros((3, d))
+        # one rounding to bf16, fp32 sums of n terms
+        tol = 2.0 ** -8 * np.abs(ref) + (n + 1) * 2.0 ** -23 * (rows.abs().mean(0).numpy() if len(rows) else 0)
+        assert np.all(np.abs(f64(mean[b]) - ref) <= tol)
+    for sparse in (False, True):
+        out = layer.draft(q.cuda(), kn.cuda(), vn.cuda(), cuda(par), sparse=sparse)
+        idx = layer.idx.cpu().numpy() if sparse else None
+        cnt = layer.count.cpu().numpy() if sparse else None
+        if not n:
+            assert out.shape == (3, 0, 3, d)
+            continue
+        ref, mag = C.tree_attend(f64(q), f64(c.k), f64(c.v), c.table, c.lens, par.tolist(), d ** -0.5, -1,
+                                 idx, cnt)
+        check_close(f64(out), ref, mag, weight_slack(f64(q), f64(c.k), d ** -0.5, 264))
+    assert J.device_error() & ~16 == 0

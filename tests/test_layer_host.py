@@ -82,3 +82,20 @@ def test_decode_refuses_other_shapes(no_launch, name, shape, with_mass):
     a[name] = torch.zeros(shape, dtype=a[name].dtype)
     with pytest.raises(ValueError, match="shape|agree"):
         api.decode(**a, budget=8, mass=torch.zeros((2, 2, 48)) if with_mass else None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), -2), (dict(batch=-1), -2), (dict(n=65), -3), (dict(n=0, mean=None), 0), (dict(batch=0), 0),
+    (dict(parents=None), -1), (dict(bt=None), -1), (dict(lens=None), -1), (dict(slots=None), -1),
+    (dict(q=None), -1), (dict(q=0x1008), -4), (dict(mean=0x6008), -4), (dict(d=96), -3), (dict(h_q=0), -2),
+    (dict(h_q=1 << 20), -3), (dict(ps=24), -3), (dict(max_pages=0), -2), (dict(num_pages=0), -2),
+])
+def test_tree_prepare_refuses(kw, status):
+    from token_level_sparse_fp8_b200 import _lib, build
+    build.build()
+    a = dict(q=0x1000, parents=0x2000, bt=0x3000, max_pages=8, lens=0x4000, batch=2, n=8, h_q=8, d=128,
+             num_pages=20, ps=16, slots=0x5000, mean=0x6000)
+    a.update(kw)
+    assert _lib.load().jssa_tree_prepare(
+        a["q"], a["parents"], a["bt"], a["max_pages"], a["lens"], a["batch"], a["n"], a["h_q"], a["d"],
+        a["num_pages"], a["ps"], a["slots"], a["mean"], None) == status

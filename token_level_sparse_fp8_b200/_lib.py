@@ -77,6 +77,7 @@ SIGNATURES = {
     "jssa_tree_attend": (c_int, [P, P, P, P, P, c_int64, c_int64, c_int64, P, c_int, P, P, P, P,
                                  c_int, c_int, c_int, c_int, c_int, c_int, c_int64, c_int, c_int,
                                  c_float, P, P, c_size_t, P]),
+    "jssa_tree_prepare": (c_int, [P, P, P, c_int, P, c_int, c_int, c_int, c_int, c_int64, c_int, P, P, P]),
     "jssa_tree_commit": (c_int, [P, P, c_int64, c_int64, c_int64, P, c_int, P, c_int, P, P, P, c_int,
                                  c_int, c_int, c_int, c_int64, c_int, P, P]),
     "jssa_indexed_attend_noalloc": (c_int, [P, P, P, c_int64, c_int64, c_int64, P, c_int, P, P, c_int,

@@ -808,6 +808,23 @@ def tree_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return out
 
 
+def _tree_prepare(q, parents, block_table, seq_lens, num_pages, page_size, mean):
+    """(slots int64 ``[batch * n]``, mean query bf16 ``[batch, h_q, d]`` or None) of a tree's used
+    nodes; the slot of any other node is -1."""
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, n, h_q, d]")
+    batch, n, h_q, d = q.shape
+    bt, max_pages = _table(block_table, "block_table", batch, q)
+    lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
+    par = _arg(parents, "parents", torch.int32, (batch, n), q)
+    slots = seq_lens.new_empty((batch * n,), dtype=torch.int64)
+    q_mean = q.new_empty((batch, h_q, d)) if mean else None
+    _call_on(q.get_device(), "jssa_tree_prepare", q.data_ptr(), par, bt, max_pages, lens, batch, n, h_q,
+             d, num_pages, page_size, slots.data_ptr(), _ptr(q_mean))
+    return slots, q_mean
+
+
 def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                 seq_lens: torch.Tensor, path: torch.Tensor, n_path: torch.Tensor,
                 score_cache: Optional[torch.Tensor] = None,
@@ -940,31 +957,16 @@ class PagedLayer:
         batch, n, h_kv, d = k_new.shape
         if n > TREE_MAX_NODES:
             raise ValueError(f"a tree has at most {TREE_MAX_NODES} nodes")
-        slots = self._node_slots(parents)
-        store(k_new.view(batch * n, h_kv, d), slots.view(-1), self.basis, self.score_cache)
+        slots, mean = _tree_prepare(q, parents, self.block_table, self.seq_lens, self.k_cache.shape[0],
+                                    self.page_size, sparse)
+        store(k_new.view(batch * n, h_kv, d), slots, self.basis, self.score_cache)
         idx = count = None
         if sparse:
-            used = (parents >= -1).to(torch.float32)
-            mean = (torch.einsum("bnhd,bn->bhd", q.float(), used)
-                    / used.sum(1).clamp(min=1.0)[:, None, None]).to(torch.bfloat16)
             idx, count = score_topk(mean, self.basis, self.score_cache, self.block_table,
                                     self.seq_lens, self.budget, self.idx, self.count,
                                     _CallWorkspace(q.device))
         return tree_attend(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens, parents,
                            k_new, v_new, idx, count, self.scale, window, out)
-
-    def _node_slots(self, parents):
-        """Flat cache slots of the tree's nodes (int64 ``[batch, n]``; -1 where a node is unused
-        or beyond the block table)."""
-        n = parents.shape[1]
-        max_pages = self.block_table.shape[1]
-        # (a negative length counts as 0, as in the library, which flags it)
-        pos = (self.seq_lens.long().clamp(min=0)[:, None]
-               + torch.arange(n, device=parents.device)[None])
-        ok = (parents >= -1) & (pos < max_pages * self.page_size)
-        page = torch.gather(self.block_table, 1,
-                            (pos // self.page_size).clamp(max=max_pages - 1)).long()
-        return torch.where(ok, page * self.page_size + pos % self.page_size, -1)
 
     def commit(self, path, n_path):
         """Keep the accepted nodes ``path[b, :n_path[b]]`` of the last drafted tree

@@ -640,6 +640,30 @@ int jssa_tree_attend(const jssa_bf16* q, const jssa_bf16* k_new, const jssa_bf16
   return cuda_status(jssa::launch_tree(a, as_stream(stream)));
 }
 
+int jssa_tree_prepare(const jssa_bf16* q, const int32_t* parents, const int32_t* block_table,
+                      int max_pages, const int32_t* seq_lens, int batch, int n_nodes, int h_q, int d,
+                      int64_t num_pages, int page_size, int64_t* slots, jssa_bf16* q_mean,
+                      jssa_stream_t stream) {
+  if (batch < 0 || n_nodes < 0) return JSSA_ERR_SHAPE;
+  if (n_nodes > jssa::kTreeMaxNodes) return JSSA_ERR_UNSUPPORTED;
+  int st = check_paging(max_pages, num_pages, page_size);
+  if (st) return st;
+  if (q_mean) {
+    if (h_q <= 0) return JSSA_ERR_SHAPE;
+    if (!supported_d(d)) return JSSA_ERR_UNSUPPORTED;
+    if ((int64_t)h_q * d > (int64_t)65535 * 1024) return JSSA_ERR_UNSUPPORTED;  // grid rows of 1024
+  }
+  if (batch == 0 || (n_nodes == 0 && !q_mean)) return JSSA_OK;
+  if (!block_table || !seq_lens || (n_nodes > 0 && (!parents || !slots || (q_mean && !q))))
+    return JSSA_ERR_NULL;
+  if (q_mean && (!aligned16(q) || !aligned16(q_mean))) return JSSA_ERR_ALIGN;
+  jssa::TreeArgs a = {};
+  a.q = q; a.block_table = block_table; a.max_pages = max_pages; a.seq_lens = seq_lens;
+  a.parents = parents; a.batch = batch; a.n = n_nodes; a.h_q = h_q; a.d = d;
+  a.num_pages = num_pages; a.page_size = page_size;
+  return cuda_status(jssa::launch_tree_prepare(a, slots, q_mean, as_stream(stream)));
+}
+
 static int check_mla_kv(const jssa_bf16* q, const void* kv_cache, int64_t kv_page_stride,
                         int64_t kv_slot_stride, const jssa_bf16* out) {
   if (!q || !kv_cache || !out) return JSSA_ERR_NULL;

@@ -125,6 +125,8 @@ struct TreeArgs {
 };
 size_t tree_ws_bytes(int batch, int n, int h_q, int h_kv, int d);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
+// Slots of the used nodes and the mean of their queries (null: not wanted).
+cudaError_t launch_tree_prepare(const TreeArgs& a, int64_t* slots, uint16_t* mean, cudaStream_t s);
 
 // Moves of cached rows (K, V, scoring codes, mass): the accepted nodes of a tree to consecutive
 // positions, and the kept positions of an eviction to the front of a page table.

@@ -118,14 +118,15 @@ struct Tree {
     return node < 32 ? lo : hi;
   }
 };
-__device__ __forceinline__ Tree tree_of(const TreeArgs& a, int b, int lane, bool report) {
+// (parents: the n parents of one sequence)
+__device__ __forceinline__ Tree tree_of(const int32_t* parents, int n, int lane, bool report) {
   Tree t;
   int ptr[2];
   bool bad[2], named[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = lane + 32 * u;
-    const int p = i < a.n ? a.parents[(int64_t)b * a.n + i] : -2;
+    const int p = i < n ? parents[i] : -2;
     t.see[u] = 1ull << i;
     named[u] = p >= -1;
     bad[u] = p < -1 || p >= i;
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
         const Pair p = pair_of(a, pair);
         const int t1 = (int)min((int64_t)p.tiles, t0 + todo - k0);
         if (lane == 0 && a.seq_lens[p.b] != p.L) raise_flag(4u);
-        const Tree tree = tree_of(a, p.b, lane, true);
+        const Tree tree = tree_of(a.parents + (int64_t)p.b * a.n, a.n, lane, true);
         if (a.k_new) {
           int64_t to[2];  // of nodes lane and lane + 32
 #pragma unroll
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO>::kThreads, 1)
         for (int u = 0; u < D / 64; ++u) prefetch_l1(qrow + 8 * u);
       const Pair p = pair_of(a, pair);
       const int t1 = (int)min((int64_t)p.tiles, t0 + todo - k0);
-      const Tree tree = tree_of(a, p.b, lane, false);
+      const Tree tree = tree_of(a.parents + (int64_t)p.b * a.n, a.n, lane, false);
       uint64_t see = tree.of(node);
       if (r >= rows) see = 0ull;
       const bool used = see != 0ull;
@@ -1012,6 +1013,49 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
                    pack_bf16x2(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
 }
 
+// What a draft needs before its attention: the cache slots of the used nodes, and the mean of their
+// queries (fp32 sums, rounded once). Block (b, x): kPrepareThreads x 8 elements of the mean of sequence
+// b, x = 0 also its slots. Unused nodes' rows are not read. Latency-bound: one chain of parents, tree and
+// rows.
+constexpr int kPrepareThreads = 128;
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(TreeArgs a, int64_t* slots, uint16_t* mean) {
+  __shared__ uint64_t s_used;
+  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
+  if (tid < 32) {
+    const Tree tree = tree_of(a.parents + (int64_t)b * a.n, a.n, lane, false);
+    const unsigned lo = __ballot_sync(kAll, tree.see[0] != 0ull), hi = __ballot_sync(kAll, tree.see[1] != 0ull);
+    if (lane == 0) s_used = (uint64_t)hi << 32 | lo;
+  }
+  __syncthreads();
+  const uint64_t used = s_used;
+  if (blockIdx.y == 0 && tid < a.n) {
+    const int max_len = a.max_pages * a.page_size;
+    const int pos = min(max(a.seq_lens[b], 0), max_len) + tid;
+    int64_t slot = -1;
+    if ((used >> tid & 1ull) && pos < max_len) {
+      const int pg = a.block_table[(int64_t)b * a.max_pages + pos / a.page_size];
+      if (pg >= 0 && (int64_t)pg < a.num_pages) slot = (int64_t)pg * a.page_size + pos % a.page_size;
+    }
+    slots[(int64_t)b * a.n + tid] = slot;
+  }
+  const int width = a.h_q * a.d, e = (blockIdx.y * kPrepareThreads + tid) * 8;
+  if (!mean || e >= width) return;
+  const uint16_t* q = a.q + (int64_t)b * a.n * width + e;
+  float2 sum[4] = {};
+#pragma unroll 4
+  for (uint64_t left = used; left; left &= left - 1) {
+    const uint4 x = *reinterpret_cast<const uint4*>(q + (int64_t)(__ffsll((long long)left) - 1) * width);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum[u] = add2(sum[u], make_float2(bf16_lo(w[u]), bf16_hi(w[u])));
+  }
+  const float n = (float)max(__popcll(used), 1);
+  uint32_t w[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) w[u] = pack_bf16x2(sum[u].x / n, sum[u].y / n);
+  *reinterpret_cast<uint4*>(mean + (int64_t)b * width + e) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <int D, bool TWO>
 cudaError_t launch_t(const TreeArgs& a, const Plan& plan, cudaStream_t s) {
   using C = Cfg<D, TWO>;
@@ -1048,6 +1092,14 @@ size_t tree_ws_bytes(int batch, int n, int h_q, int h_kv, int d) {
   const Plan p = plan_tree(n, h_q / h_kv, d);
   const size_t rows = 2 * (size_t)p.ctas * p.slot_rows;
   return up256(p.ctas * sizeof(int2)) + up256(rows * sizeof(float2)) + rows * d * sizeof(float);
+}
+
+cudaError_t launch_tree_prepare(const TreeArgs& a, int64_t* slots, uint16_t* mean, cudaStream_t s) {
+  using namespace tree_detail;
+  if (a.batch == 0 || (a.n == 0 && !mean)) return cudaSuccess;
+  const int per = kPrepareThreads * 8;
+  prepare_kernel<<<dim3(a.batch, mean ? (a.h_q * a.d + per - 1) / per : 1), kPrepareThreads, 0, s>>>(a, slots, mean);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
