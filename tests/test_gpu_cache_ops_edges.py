@@ -236,3 +236,31 @@ def test_draft_sizes(n, d, r):
                                  idx, cnt)
         check_close(f64(out), ref, mag, weight_slack(f64(q), f64(c.k), d ** -0.5, 264))
     assert J.device_error() & ~16 == 0
+
+
+def test_a_refused_draft_changes_nothing():
+    J = jssa()
+    c, layer = make_layer([300, 120], extra=80, seed=75)
+    q, kn, vn = c.normal(2, 6, 8, 128).cuda(), c.normal(2, 6, 2, 128).cuda(), c.normal(2, 6, 2, 128).cuda()
+    par = cuda([random_tree(c.rng, 6) for _ in range(2)])
+    layer.idx.fill_(3), layer.count.fill_(4)
+    state = [c.k, c.v, layer.score_cache, layer.seq_lens, layer.idx, layer.count, layer.mass]
+    before = [t.clone() for t in state]
+    for sparse in (False, True):
+        wide = c.normal(2, 6, 2, 256).cuda()
+        for args, kw in [
+            ((q, kn, vn, par.long()), {}), ((q, kn, vn, par.cpu()), {}), ((q, kn, vn, par[:, :5]), {}),
+            ((q[:, :5], kn, vn, par), {}), ((q.float(), kn, vn, par), {}), ((q, kn, vn.float(), par), {}),
+            ((q, kn, vn[:, :, :1], par), {}), ((q, kn[:1], vn, par), {}), ((q, kn, None, par), {}),
+            ((q, wide, wide, par), {}), ((q[0], kn, vn, par), {}),
+            ((q, kn.transpose(1, 2).contiguous().transpose(1, 2), vn, par), {}),
+            ((q, kn, vn, par), dict(out=torch.empty_like(q)[:1])),
+            ((q.repeat(1, 1, 5, 1), kn, vn, par), {}),  # 20 query heads per KV head
+            ((q[:, :, :3].contiguous(), kn, vn, par), {}),  # 3 query heads, 2 KV heads
+            *([((q, kn, vn, par), dict(window=32))] if sparse else []),
+        ]:
+            with pytest.raises((ValueError, TypeError, J.JSSAError)):
+                layer.draft(*args, sparse=sparse, **kw)
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(state, before))
+    assert J.device_error() == 0

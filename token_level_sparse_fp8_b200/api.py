@@ -769,6 +769,12 @@ def tree_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     node ``p``, below -1 marks an unused (padded) node, whose output is zero. A node sees itself,
     its ancestors and the committed tokens: all of them, a sliding ``window`` ending at its own
     logical position, or the index set ``idx`` / ``count`` of :func:`score_topk`."""
+    t = _tree_check(q, k_cache, v_cache, block_table, seq_lens, parents, k_new, v_new, out)
+    return _tree_run(t, idx, count, scale, window, ws)
+
+
+def _tree_check(q, k_cache, v_cache, block_table, seq_lens, parents, k_new, v_new, out):
+    """Checks the arguments of a tree call; what :func:`_tree_run` needs of them."""
     _need(q, "q", torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [batch, n, h_q, d]")
@@ -786,6 +792,16 @@ def tree_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if k_new is not None:
         kn = _arg(k_new, "k_new", torch.bfloat16, (batch, n, h_kv, d), q)
         vn = _arg(v_new, "v_new", torch.bfloat16, (batch, n, h_kv, d), q)
+    if out is not None:
+        _arg(out, "out", torch.bfloat16, q.shape, q)
+    nbytes = _ws_bytes(FN_TREE_ATTEND, batch, h_q, h_kv, d, max_pages, page_size, n, index)
+    return (q, out, (q.data_ptr(), kn, vn, *kv, *strides, bt, max_pages, lens, par),
+            (batch, n, h_q, h_kv, d), (num_pages, page_size), nbytes)
+
+
+def _tree_run(t, idx, count, scale, window, ws):
+    q, out, tensors, sizes, paging, nbytes = t
+    batch, _, _, h_kv, d = sizes
     if (idx is None) != (count is None):
         raise ValueError("idx and count go together")
     i = c = None
@@ -798,30 +814,21 @@ def tree_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _arg(out, "out", torch.bfloat16, q.shape, q)
-    p, nb, _hold = _scratch(ws, _ws_bytes(FN_TREE_ATTEND, batch, h_q, h_kv, d, max_pages, page_size,
-                                          n, index), q)
-    _call_on(index, "jssa_tree_attend", q.data_ptr(), kn, vn, *kv, *strides, bt, max_pages, lens,
-             par, i, c, batch, n, h_q, h_kv, d, budget, num_pages, page_size, window, scale,
-             out.data_ptr(), p, nb)
+    p, n, _hold = _scratch(ws, nbytes, q)
+    _call_on(q.get_device(), "jssa_tree_attend", *tensors, i, c, *sizes, budget, *paging, window, scale,
+             out.data_ptr(), p, n)
     return out
 
 
 def _tree_prepare(q, parents, block_table, seq_lens, num_pages, page_size, mean):
     """(slots int64 ``[batch * n]``, mean query bf16 ``[batch, h_q, d]`` or None) of a tree's used
-    nodes; the slot of any other node is -1."""
-    _need(q, "q", torch.bfloat16)
-    if q.dim() != 4:
-        raise ValueError("q must be [batch, n, h_q, d]")
+    nodes; the slot of any other node is -1. The arguments have been checked (:func:`_tree_check`)."""
     batch, n, h_q, d = q.shape
-    bt, max_pages = _table(block_table, "block_table", batch, q)
-    lens = _arg(seq_lens, "seq_lens", torch.int32, (batch,), q)
-    par = _arg(parents, "parents", torch.int32, (batch, n), q)
     slots = seq_lens.new_empty((batch * n,), dtype=torch.int64)
     q_mean = q.new_empty((batch, h_q, d)) if mean else None
-    _call_on(q.get_device(), "jssa_tree_prepare", q.data_ptr(), par, bt, max_pages, lens, batch, n, h_q,
-             d, num_pages, page_size, slots.data_ptr(), _ptr(q_mean))
+    _call_on(q.get_device(), "jssa_tree_prepare", q.data_ptr(), parents.data_ptr(), block_table.data_ptr(),
+             block_table.shape[1], seq_lens.data_ptr(), batch, n, h_q, d, num_pages, page_size,
+             slots.data_ptr(), _ptr(q_mean))
     return slots, q_mean
 
 
@@ -954,19 +961,29 @@ class PagedLayer:
         (:func:`tree_attend`); the nodes' K, V and scoring codes are stored at positions
         ``seq_lens[b] + i``. ``sparse``: the context is the top-B selection of the mean query of
         the tree's used nodes, one set per KV head for the whole tree."""
-        batch, n, h_kv, d = k_new.shape
-        if n > TREE_MAX_NODES:
+        index = self.k_cache.get_device()
+        if torch._C._cuda_getDevice() != index:
+            with torch.cuda.device(index):
+                return self.draft(q, k_new, v_new, parents, out, window, sparse)
+        if k_new is None or v_new is None:
+            raise ValueError("a draft stores its nodes: k_new and v_new are needed")
+        if q.dim() == 4 and q.shape[1] > TREE_MAX_NODES:
             raise ValueError(f"a tree has at most {TREE_MAX_NODES} nodes")
+        if sparse and window > 0:
+            raise ValueError("a draft has a window or a selected context, not both")
+        # (everything is checked before anything is stored)
+        t = _tree_check(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens, parents, k_new,
+                        v_new, out)
         slots, mean = _tree_prepare(q, parents, self.block_table, self.seq_lens, self.k_cache.shape[0],
                                     self.page_size, sparse)
-        store(k_new.view(batch * n, h_kv, d), slots, self.basis, self.score_cache)
         idx = count = None
         if sparse:
             idx, count = score_topk(mean, self.basis, self.score_cache, self.block_table,
                                     self.seq_lens, self.budget, self.idx, self.count,
                                     _CallWorkspace(q.device))
-        return tree_attend(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens, parents,
-                           k_new, v_new, idx, count, self.scale, window, out)
+        out = _tree_run(t, idx, count, self.scale, window, None)
+        store(k_new.view(-1, *k_new.shape[2:]), slots, self.basis, self.score_cache)
+        return out
 
     def commit(self, path, n_path):
         """Keep the accepted nodes ``path[b, :n_path[b]]`` of the last drafted tree
