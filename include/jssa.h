@@ -454,9 +454,10 @@ JSSA_API int jssa_decode_mass(const jssa_bf16* q, const jssa_bf16* k_new, const 
  * positions). Nothing else is written.
  * dst_block_table, int32 [batch, dst_max_pages]: block_table itself (the same pointer) moves the rows
  * in place, which needs pages that no other sequence shares; any other table must name pages that this
- * call reads for no sequence (for instance when the source pages are shared). mass_out may be mass. Positions of dst_block_table beyond its end or its
- * unusable pages are skipped and flagged, as are unusable source pages (the destination row is left
- * as it was). 1 <= keep, 0 <= recent <= keep; lens_out must not be seq_lens, nor idx, count and
+ * call reads for no sequence (for instance when the source pages are shared). mass_out is mass itself
+ * or memory that does not overlap it. Positions of dst_block_table beyond its end or its unusable pages
+ * are skipped and flagged, as are unusable source pages (the destination row is left as it was, its
+ * mass too). 1 <= keep, 0 <= recent <= keep; lens_out must not be seq_lens, nor idx, count and
  * lens_out overlap an input. score_bytes: bytes of one scoring row (16, 32 or 64: r, or 2 r for a
  * bf16 scoring cache), the scoring cache as in the conventions. mass, mass_out: float32, rows of
  * mass_stride elements as in jssa_dense_decode_mass. No workspace.

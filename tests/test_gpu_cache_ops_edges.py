@@ -264,3 +264,62 @@ def test_a_refused_draft_changes_nothing():
             torch.cuda.synchronize()
             assert all(torch.equal(x, y) for x, y in zip(state, before))
     assert J.device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------------
+# eviction and commit over unusable pages
+# ------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("L,keep", [(100, 40), (3000, 700)])
+@pytest.mark.parametrize("how", ["in place", "mass apart", "pages apart", "both apart"])
+def test_evict_leaves_rows_of_unusable_pages_alone(how, L, keep):
+    # a row that cannot be read or written stays as it was: K, V, code and mass
+    J = jssa()
+    ps, h_kv = 16, 2
+    c = Paged([1, 1], 0, h_kv, 128, ps, pages=-(-L // ps), seed=keep)
+    lens = cuda([L, L - 7])
+    c.k.copy_(c.normal(*c.k.shape)), c.v.copy_(c.normal(*c.v.shape))
+    n0, per = c.k.shape[0], -(-keep // ps)
+    if "pages" in how or "both" in how:
+        c.k, c.v = (torch.cat([t, torch.zeros((2 * per, *t.shape[1:]), dtype=t.dtype, device="cuda")])
+                    for t in (c.k, c.v))
+    codes = torch.randint(0, 256, (c.k.shape[0], h_kv, ps, 32), dtype=torch.uint8, device="cuda")
+    mass = torch.rand((2, h_kv, c.table.shape[1] * ps), device="cuda") ** 6
+    src = c.table.copy()
+    src[0, 3], src[1, 1], src[1, 5] = -1, 10 ** 6, c.k.shape[0]
+    if c.k.shape[0] == n0:
+        dst = src
+    else:
+        dst = (n0 + np.arange(2 * per)).reshape(2, per)
+        dst[0, 1] = -5
+        dst = dst[:, :-1]  # (one page short: the last rows have no place)
+    apart = how in ("mass apart", "both apart")
+    mass_out = torch.full_like(mass, 5.0) if apart else mass
+    start = [t.clone() for t in (c.k, c.v, codes, mass, mass_out)]
+    bt = cuda(src)
+    idx, count, _ = J.evict(mass, c.k, c.v, bt, lens, keep, 9, codes,
+                            None if dst is src else cuda(dst), mass_out if apart else None)
+    assert J.device_error() == (1 if dst is src else 3)
+    k1, v1, s1, _, m1 = (t.clone().cpu() for t in start)
+    k0, v0, s0, m0, _ = (t.cpu() for t in start)
+
+    def place(table, b, t):
+        page = table[b, t // ps] if t // ps < table.shape[1] else -1
+        return (page, t % ps) if 0 <= page < c.k.shape[0] else None
+
+    for b, n in enumerate([L, L - 7]):
+        for h in range(h_kv):
+            want = C.kept_positions(m0[b, h].numpy(), n, keep, 9)
+            assert np.array_equal(idx[b, h].cpu().numpy(), want)
+            for i, t in enumerate(want):
+                a, z = place(src, b, t), place(dst, b, i)
+                if a is None or z is None:
+                    continue
+                k1[z[0], z[1], h], v1[z[0], z[1], h] = k0[a[0], a[1], h], v0[a[0], a[1], h]
+                s1[z[0], h, z[1]], m1[b, h, i] = s0[a[0], h, a[1]], m0[b, h, t]
+            m1[b, h, keep:n] = 0
+    for got, ref in zip((c.k, c.v, codes, mass_out), (k1, v1, s1, m1)):
+        assert torch.equal(got.cpu(), ref)
+    if apart:
+        assert torch.equal(mass.cpu(), m0)

@@ -93,7 +93,7 @@ struct WarpTile {
       if (u < kRows && pg >= 0)
         code = *reinterpret_cast<const uint4*>(m.score_cache + code_offset(m, pg, pos, h) + (lane % per) * 16);
     }
-    if (mass_row && lane < kRows && e.src_pos >= 0) mass = mass_row[e.src_pos];
+    if (mass_row && lane < kRows && e.src_pg >= 0) mass = mass_row[e.src_pos];
   }
   __device__ __forceinline__ void store(const RowMove& m, int h, float* mass_row, const Ends& e,
                                         int lane) const {
@@ -108,7 +108,7 @@ struct WarpTile {
       if (u < kRows && pg >= 0)
         *reinterpret_cast<uint4*>(m.score_cache + code_offset(m, pg, pos, h) + (lane % per) * 16) = code;
     }
-    if (mass_row && lane < kRows && e.src_pos >= 0) mass_row[e.dst_pos] = mass;
+    if (mass_row && lane < kRows && e.dst_pg >= 0) mass_row[e.dst_pos] = mass;
   }
 };
 
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(RowMove m, EvictArgs
   read(x[0], 0);
   // mass: lane u's row; scoring codes: 16-byte chunks, `per` of a row side by side
   const float mass = src >= 0 ? e.mass[(int64_t)pair * e.mass_stride + src] : 0.f;
-  if (src >= 0) e.mass_out[(int64_t)pair * e.mass_stride + i] = mass;
+  if (to >= 0) e.mass_out[(int64_t)pair * e.mass_stride + i] = mass;
 #pragma unroll 1
   for (int g = 0; g < 32 / kGroup; g += 2) {
     read(x[1], g + 1);
