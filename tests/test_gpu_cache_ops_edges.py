@@ -323,3 +323,18 @@ def test_evict_leaves_rows_of_unusable_pages_alone(how, L, keep):
         assert torch.equal(got.cpu(), ref)
     if apart:
         assert torch.equal(mass.cpu(), m0)
+
+
+@pytest.mark.parametrize("node", [1, 2])
+def test_commit_flags_an_accepted_node_on_an_unusable_page(node):
+    # a node that keeps its position is an entry like any other
+    J = jssa()
+    c = Paged([15, 40], 20, 1, seed=80)
+    table = c.table.copy()
+    table[0, 1] = -1  # (positions 16.. of the first sequence: its nodes 1..)
+    path = np.array([[0, 0, 0], [0, 1, 2]])
+    path[0, 1] = node
+    k0 = c.k.clone()
+    out = J.tree_commit(c.k, c.v, cuda(table), c.seq_lens, cuda(path), cuda([2, 3]))
+    assert J.device_error() == 1 and out.tolist() == [17, 43]
+    assert torch.equal(torch.nan_to_num(c.k, nan=7.0), torch.nan_to_num(k0, nan=7.0))

@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(kCommitThreads)
     const int node = path[(int64_t)b * max_path + i];
     if (node < 0 || node >= kTreeMaxNodes) {
       raise_flag(2u);
-    } else if (node != i) {
+    } else {  // (a node that keeps its position only has its page checked)
       const int sp = page_of(m, table, m.max_pages, L + node);
-      const int dp = page_of(m, table, m.max_pages, L + i);
+      const int dp = node != i ? page_of(m, table, m.max_pages, L + i) : -1;
       if (sp >= 0 && dp >= 0) ends = {L + node, L + i, sp, dp};
     }
   }
