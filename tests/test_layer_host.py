@@ -99,3 +99,12 @@ def test_tree_prepare_refuses(kw, status):
     assert _lib.load().jssa_tree_prepare(
         a["q"], a["parents"], a["bt"], a["max_pages"], a["lens"], a["batch"], a["n"], a["h_q"], a["d"],
         a["num_pages"], a["ps"], a["slots"], a["mean"], None) == status
+
+
+def test_host_pipeline_refuses_a_layer_that_keeps_the_mass():
+    # its steps would leave the mass behind, and a later eviction would go by stale sums
+    class Layer:
+        mass = torch.zeros((1, 1, 16))
+
+    with pytest.raises(ValueError, match="mass"):
+        api.HostPipeline(Layer(), (1, 4, 128), (1, 1, 128))

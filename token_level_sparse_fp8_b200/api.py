@@ -1012,9 +1012,11 @@ class HostPipeline:
     running while the previous step computes and its download while the next one does (two
     staging sets and two copy streams inside the library, ordered by events). Steps run on the
     CUDA stream that is current when the pipeline is built. Calls are asynchronous: a step's
-    output is in its host buffer, and its host inputs may be rewritten, after ``synchronize``."""
+    output is in its host buffer, and its host inputs may be rewritten, after ``synchronize``. A
+    layer that tracks the attention mass is refused: these steps do not add to it."""
 
     def __init__(self, layer: "PagedLayer", q_shape, kv_new_shape):
+        self._no_mass(layer)
         dev = layer.k_cache.device
         batch, h_q, d = q_shape
         num_pages, page_size, h_kv, _ = layer.k_cache.shape
@@ -1039,6 +1041,12 @@ class HostPipeline:
         # address, its next step orders its copies after the work already on the stream again
         call("jssa_decode_host_join", ws_p, self._stream)
 
+    @staticmethod
+    def _no_mass(layer):
+        if layer.mass is not None:
+            raise ValueError("a HostPipeline's steps do not add to a layer's mass: build the layer "
+                             "without track_mass, or call its step")
+
     def _host(self, t, name, shape):
         if not isinstance(t, torch.Tensor) or t.device.type != "cpu" or t.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be a bf16 tensor in host memory")
@@ -1046,6 +1054,7 @@ class HostPipeline:
             raise ValueError(f"{name} must be contiguous with shape {shape}")
 
     def step(self, q_host, k_new_host, v_new_host, out_host):
+        self._no_mass(self.layer)
         self._host(q_host, "q_host", self._q_shape)
         self._host(out_host, "out_host", self._q_shape)
         if (k_new_host is None) != (v_new_host is None):
