@@ -410,7 +410,8 @@ JSSA_API int jssa_decode_host_join(const void* ws, jssa_stream_t stream);
  * mass + (b*h_kv + h)*mass_stride, mass_stride >= max_pages*page_size (JSSA_ERR_SHAPE otherwise).
  * Scores and sums are fp32. All other arguments, the output and the errors as in the call without
  * mass (jssa_dense_decode, jssa_indexed_attend, jssa_decode). An index set that names a position
- * twice is not allowed (its sum would be undefined). ws: >= jssa_workspace_size of
+ * twice is not allowed (its sum would be undefined), nor are two calls at once on one mass (an entry is
+ * read, added to and written back: sums would be lost). ws: >= jssa_workspace_size of
  * JSSA_FN_DENSE_DECODE_MASS, JSSA_FN_INDEXED_ATTEND_MASS or JSSA_FN_DECODE_MASS, 16-byte aligned:
  * partial outputs and h_q*4 bytes of scores per attended position; no clearing needed.
  */

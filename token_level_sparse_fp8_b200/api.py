@@ -477,7 +477,7 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     """Gather-free attention of every query head over its KV head's index set. With ``mass``
     (float32 ``[batch, h_kv, >= max_pages * page_size]``) every attended position's weight, summed
     over the KV head's query heads, is added to its entry (an index set then names no position
-    twice)."""
+    twice, and no other call adds to the same mass at the same time)."""
     if mass is not None:
         return _attend_mass(q, k_cache, v_cache, block_table, mass, scale, out, ws, idx=idx, count=count)
     _need(q, "q", torch.bfloat16)
@@ -911,7 +911,11 @@ class PagedLayer:
     ``commit`` run a tree of drafted tokens and keep its accepted path; with ``track_mass`` every
     ``step`` and ``dense`` adds the positions' attention weights to ``mass``, and ``evict`` cuts
     the cache down by them. ``seq_lens`` is updated in place by ``commit`` and ``evict`` and
-    otherwise belongs to the caller."""
+    otherwise belongs to the caller: ``draft`` and ``commit`` take it as the number of committed
+    tokens (the nodes lie behind them), ``step`` as counting the token it stores, at position
+    ``seq_lens - 1``, so the caller adds 1 before a step. ``draft`` and ``commit`` add nothing to
+    ``mass``: after a loop of them alone an eviction keeps the oldest positions (ties) beside the
+    ``recent`` ones."""
 
     def __init__(self, k_cache, v_cache, block_table, seq_lens, basis, budget, scale=None,
                  track_mass=False):
