@@ -108,3 +108,16 @@ def test_host_pipeline_refuses_a_layer_that_keeps_the_mass():
 
     with pytest.raises(ValueError, match="mass"):
         api.HostPipeline(Layer(), (1, 4, 128), (1, 1, 128))
+
+
+def test_decode_accepts_caches_with_more_pages(monkeypatch):
+    # a pool of codes or values that is larger than K's holds every row the call names
+    reached = []
+    monkeypatch.setattr(api, "_need", lambda *a, **k: None)
+    monkeypatch.setattr(api, "_ws", lambda *a, **k: reached.append(1) or (_ for _ in ()).throw(KeyError))
+    a = _decode_args()
+    a["v_cache"] = torch.zeros((9, 16, 2, 128), dtype=torch.bfloat16)
+    a["score_cache"] = torch.zeros((7, 2, 16, 32), dtype=torch.uint8)
+    with pytest.raises(KeyError):
+        api.decode(**a, budget=8)
+    assert reached

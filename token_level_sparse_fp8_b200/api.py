@@ -208,8 +208,10 @@ def _mass(t: torch.Tensor, name: str, batch: int, h_kv: int, capacity: int, like
 
 
 def _head_dim(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor):
-    """The kernels read ``d`` elements of a cache row, ``d`` from the query: both caches must have it."""
-    if k_cache.shape[-1] != q.shape[-1] or v_cache.shape != k_cache.shape:
+    """The kernels read ``d`` elements of a cache row, ``d`` from the query, and as many pages of V as
+    K has: both caches must hold them."""
+    if (k_cache.shape[-1] != q.shape[-1] or v_cache.shape[1:] != k_cache.shape[1:]
+            or v_cache.shape[0] < k_cache.shape[0]):
         raise ValueError(f"the caches must agree with the head dim {q.shape[-1]} of q and with each "
                          f"other, got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
 
@@ -711,7 +713,7 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
     for t, n, shape in ((basis, "basis", (h_kv, r, d)),
                         (score_cache, "score_cache", (num_pages, h_kv, page_size, r)),
                         (k_new, "k_new", (batch, h_kv, d)), (v_new, "v_new", (batch, h_kv, d))):
-        if t is not None and t.shape != shape:
+        if t is not None and (t.shape[1:] != shape[1:] or t.shape[0] < shape[0]):
             raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
     strides = kv_strides(k_cache)
     if kv_strides(v_cache) != strides:
