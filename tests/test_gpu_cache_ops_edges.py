@@ -338,3 +338,186 @@ def test_commit_flags_an_accepted_node_on_an_unusable_page(node):
     out = J.tree_commit(c.k, c.v, cuda(table), c.seq_lens, cuda(path), cuda([2, 3]))
     assert J.device_error() == 1 and out.tolist() == [17, 43]
     assert torch.equal(torch.nan_to_num(c.k, nan=7.0), torch.nan_to_num(k0, nan=7.0))
+
+
+# ------------------------------------------------------------------------------------------------
+# rarer branches: groups, head dims, many splits, long contexts, non-finite values in later tiles
+# ------------------------------------------------------------------------------------------------
+
+
+def _ref_attend(q, k, v, table, positions, h, g, scale, mass=None):
+    """Float64 on the GPU: (outputs [g, d], sum of weight * |v|, weights summed over the group) of the
+    query heads of KV head ``h`` over ``positions`` (a tensor)."""
+    ps = k.shape[1]
+    page = table.long()[positions // ps]
+    kk, vv = k[page, positions % ps, h].double(), v[page, positions % ps, h].double()
+    p = torch.softmax(q[h * g:(h + 1) * g].double() @ kk.T * scale, 1)
+    return p @ vv, p @ vv.abs(), p.sum(0)
+
+
+def check_mass_call(out, mass, before, q, k, v, bt, positions, g, scale):
+    """``positions(b, h)``: the attended positions. Outputs and masses of a call against float64: a
+    weight is off by the slack without its split, which the masses do not have."""
+    batch, h_kv, d = q.shape[0], k.shape[2], k.shape[3]
+    for b in range(batch):
+        for h in range(h_kv):
+            pos = positions(b, h)
+            got, old = mass[b, h].double(), before[b, h].double()
+            if len(pos) == 0:
+                assert torch.count_nonzero(out[b, h * g:(h + 1) * g]).item() == 0
+                assert torch.equal(got, old)
+                continue
+            o, a, w = _ref_attend(q[b], k, v, bt[b], pos, h, g, scale)
+            qa = q[b, h * g:(h + 1) * g].double().abs()
+            top = float((qa @ k[bt[b].long()[pos // k.shape[1]], pos % k.shape[1], h].double().abs().T).max())
+            slack = 2 * (d * 2.0 ** -23 * scale * top + 2.0 ** -20) + 3 * len(pos) * 2.0 ** -23
+            tol = 2.0 ** -8 * o.abs() + (1 + 2.0 ** -8) * (slack + 2.0 ** -14) * a
+            assert bool(((out[b, h * g:(h + 1) * g].double() - o).abs() <= tol).all())
+            assert bool(((got[pos] - old[pos] - w).abs() <= slack * w + 2.0 ** -22 * (old[pos] + w)).all())
+            rest = torch.ones(len(got), dtype=torch.bool, device="cuda")
+            rest[pos] = False
+            assert torch.equal(got[rest], old[rest])
+
+
+def paged_normal(lens, h_kv, d, seed, extra=0, ps=16):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    per = -(-(max(lens) + extra) // ps)
+    total = len(lens) * per + 2
+    bt = torch.randperm(total, generator=gen, device="cuda")[:len(lens) * per].view(len(lens), per).int()
+    k, v = (torch.empty((total, ps, h_kv, d), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+            for _ in range(2))
+    return gen, bt, k, v
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("g", [1, 2, 3, 4, 5, 8])
+@pytest.mark.parametrize("budget", [70, 1100])
+def test_indexed_mass_groups_and_head_dims(budget, g, d):
+    J = jssa()
+    lens, h_kv = [0, 5, 90, 1700], 2
+    gen, bt, k, v = paged_normal(lens, h_kv, d, seed=g + d)
+    q = torch.empty((4, h_kv * g, d), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) * 2
+    idx = torch.full((4, h_kv, budget), -1, dtype=torch.int32, device="cuda")
+    count = torch.zeros((4, h_kv), dtype=torch.int32, device="cuda")
+    for b, L in enumerate(lens):
+        for h in range(h_kv):
+            m = min(L, budget - h)
+            count[b, h] = m
+            idx[b, h, :m] = torch.randperm(L, generator=gen, device="cuda")[:m].sort().values.int()
+    mass = torch.rand((4, h_kv, bt.shape[1] * 16 + 3), generator=gen, device="cuda")
+    before = mass.clone()
+    out = J.indexed_attend(q, k, v, bt, idx, count, mass=mass)
+    check_mass_call(out, mass, before, q, k, v, bt,
+                    lambda b, h: idx[b, h, :int(count[b, h])].long(), g, d ** -0.5)
+    assert J.device_error() == 0
+
+
+@pytest.mark.parametrize("d,r,g,h_kv", [(128, 16, 1, 2), (128, 64, 3, 2), (128, 32, 8, 1), (256, 64, 2, 2),
+                                        (256, 64, 4, 1)])
+def test_decode_step_with_mass(d, r, g, h_kv):
+    J = jssa()
+    lens, budget = [1, 40, 3000], 96
+    gen, bt, k, v = paged_normal(lens, h_kv, d, seed=r + g)
+    basis = torch.linalg.qr(torch.randn((h_kv, d, r), generator=gen, device="cuda"))[0].transpose(1, 2).contiguous()
+    layer = J.PagedLayer(k, v, bt, cuda(lens), basis, budget, track_mass=True)
+    layer.prefill_scores()
+    plain = J.PagedLayer(k.clone(), v.clone(), bt, cuda(lens), basis, budget)
+    plain.score_cache.copy_(layer.score_cache)
+    new = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)  # noqa: E731
+    layer.mass.copy_(torch.rand(layer.mass.shape, generator=gen, device="cuda"))
+    for _ in range(2):
+        q, kn, vn = new(3, h_kv * g, d), new(3, h_kv, d), new(3, h_kv, d)
+        before = layer.mass.clone()
+        out, idx, count = layer.step(q, kn, vn)
+        _, idx2, count2 = plain.step(q, kn, vn)
+        assert torch.equal(idx, idx2) and torch.equal(count, count2)
+        assert torch.equal(layer.k_cache, plain.k_cache) and torch.equal(layer.score_cache, plain.score_cache)
+        check_mass_call(out, layer.mass, before, q, layer.k_cache, layer.v_cache, bt,
+                        lambda b, h: idx[b, h, :int(count[b, h])].long(), g, d ** -0.5)
+    assert J.device_error() & ~16 == 0
+
+
+@pytest.mark.parametrize("d,g", [(128, 1), (128, 4), (256, 3)])
+def test_dense_mass_over_many_splits(d, g):
+    # one pair over 42K positions: more partials than the second kernel keeps weights of
+    J = jssa()
+    gen, bt, k, v = paged_normal([42001], 1, d, seed=d + g)
+    q = torch.empty((1, g, d), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) * 2
+    mass = torch.rand((1, 1, bt.shape[1] * 16), generator=gen, device="cuda")
+    for window in (-1, 40000):
+        before = mass.clone()
+        out = J.dense_decode(q, k, v, bt, cuda([42001]), window=window, mass=mass)
+        lo = 0 if window < 0 else 42001 - window
+        check_mass_call(out, mass, before, q, k, v, bt,
+                        lambda b, h: torch.arange(lo, 42001, device="cuda"), g, d ** -0.5)
+    assert J.device_error() == 0
+
+
+@pytest.mark.parametrize("batch,L,n,g,h_kv,d,window", [
+    (1, 131072, 9, 4, 1, 128, -1), (1, 131072, 64, 4, 1, 128, -1), (1, 70001, 5, 2, 2, 256, -1),
+    (2, 131072, 40, 4, 1, 128, 100000), (1, 131000, 3, 8, 1, 256, 4096),
+])
+def test_tree_attend_over_the_longest_contexts(batch, L, n, g, h_kv, d, window):
+    J = jssa()
+    lens = [L - 1009 * b for b in range(batch)]
+    gen, bt, k, v = paged_normal(lens, h_kv, d, seed=n, extra=n)
+    rng = np.random.default_rng(n)
+    q = torch.empty((batch, n, h_kv * g, d), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) * 2
+    parents = [random_tree(rng, n, b) for b in range(batch)]
+    out = J.tree_attend(q, k, v, bt, cuda(lens), cuda(parents), window=window)
+    for b in range(batch):
+        for i in range(n):
+            pos = C.tree_positions(parents[b], i, lens[b], window)
+            if not pos:
+                assert torch.count_nonzero(out[b, i]).item() == 0
+                continue
+            pos = torch.as_tensor(np.asarray(pos)).cuda()
+            for h in range(h_kv):
+                o, a, _ = _ref_attend(q[b, i], k, v, bt[b], pos, h, g, d ** -0.5)
+                qa = q[b, i, h * g:(h + 1) * g].double().abs()
+                top = float((qa @ k[bt[b].long()[pos // 16], pos % 16, h].double().abs().T).max())
+                # (a row's sums run over tiles of 64 positions, a CTA's share of them, and the CTAs' partials)
+                slack = 2.0 ** -14 + 2 * (d * 2.0 ** -23 * d ** -0.5 * top + 2.0 ** -20) + 3 * len(pos) * 2.0 ** -23
+                tol = 2.0 ** -8 * o.abs() + (1 + 2.0 ** -8) * slack * a
+                assert bool(((out[b, i, h * g:(h + 1) * g].double() - o).abs() <= tol).all())
+    assert J.device_error() == 0
+
+
+@pytest.mark.parametrize("bad", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("n,g,d", [(33, 4, 128), (64, 4, 128), (64, 8, 128), (40, 3, 128), (40, 3, 256), (64, 4, 256)])
+def test_masked_values_in_later_tiles_do_not_leak(n, g, d, bad):
+    # as test_masked_values_do_not_leak, with nodes in the fifth and sixth tile of their pair, and with
+    # more rows than one group holds
+    J = jssa()
+    L = 300
+    c = Paged([L], n, 1, d, seed=n)
+    parents = [random_tree(c.rng, n)]
+    anc = C.ancestors(parents[0])
+    depth = [len(a) - 1 for a in anc]
+    q, kn, vn = c.normal(1, n, g, d), c.normal(1, n, 1, d), c.normal(1, n, 1, d)
+    run = lambda **kw: J.tree_attend(  # noqa: E731
+        q.cuda(), c.k, c.v, c.bt, c.seq_lens, cuda(parents), kn.cuda(), vn.cuda(), **kw)[0].float()
+    ref = run()
+    for node in (2, n - 9):
+        was = vn[0, node, 0, 7].clone()
+        vn[0, node, 0, 7] = bad
+        out = run()
+        vn[0, node, 0, 7] = was
+        sees = torch.as_tensor([node in a for a in anc])
+        assert bool(sees.any()) and not bool(sees.all())
+        assert torch.equal(out[~sees], ref[~sees])
+        hit = out[sees][..., 7]
+        assert bool((torch.isnan(hit) if math.isnan(bad) else hit == bad).all())
+        out[..., 7] = ref[..., 7]
+        assert bool(torch.isfinite(out).all())
+        # (V of that tile is cleared and added by hand: the other elements are the same sums)
+        assert torch.equal(out, ref)
+    # a window that starts in a tile with a bad value, seen by the shallow nodes only
+    window = 150
+    ref = run(window=window)
+    t = L + 2 - window
+    c.v[c.table[0, t // 16], t % 16, 0, 2] = bad
+    out = run(window=window)
+    sees = torch.as_tensor([dep <= 1 for dep in depth])
+    assert torch.equal(out[~sees], ref[~sees])
+    assert not bool(torch.isfinite(out[sees][..., 2]).any())
