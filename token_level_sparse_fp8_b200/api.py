@@ -55,7 +55,7 @@ def default_rank(head_dim: int) -> int:
 
 
 def _capturing() -> bool:
-    return torch.cuda.is_current_stream_capturing()
+    return torch._C._cuda_isCurrentStreamCapturing()
 
 
 def kv_strides(cache: torch.Tensor) -> Tuple[int, int, int]:
@@ -207,13 +207,23 @@ def _mass(t: torch.Tensor, name: str, batch: int, h_kv: int, capacity: int, like
     return p, row
 
 
-def _head_dim(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor):
+def _holds(have, need) -> bool:
+    """Whether a tensor of shape ``have`` has every row of one of shape ``need``."""
+    return have[1:] == need[1:] and have[0] >= need[0]
+
+
+def _head_dim(d: int, k_cache: torch.Tensor, v_cache: torch.Tensor):
     """The kernels read ``d`` elements of a cache row, ``d`` from the query, and as many pages of V as
     K has: both caches must hold them."""
-    if (k_cache.shape[-1] != q.shape[-1] or v_cache.shape[1:] != k_cache.shape[1:]
-            or v_cache.shape[0] < k_cache.shape[0]):
-        raise ValueError(f"the caches must agree with the head dim {q.shape[-1]} of q and with each "
-                         f"other, got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    ks, vs = k_cache.shape, v_cache.shape
+    if ks[-1] != d or (vs != ks and not _holds(vs, ks)):
+        raise ValueError(f"the caches must agree with the head dim {d} of q and with each other, got "
+                         f"{tuple(ks)} and {tuple(vs)}")
+
+
+def _rows(t: torch.Tensor, name: str, shape):
+    if t.shape != shape and not _holds(t.shape, shape):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def _same_device(like: torch.Tensor, *tensors):
@@ -489,7 +499,7 @@ def indexed_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     _need(idx, "idx", torch.int32)
     _need(count, "count", torch.int32)
     batch, h_q, d = q.shape
-    _head_dim(q, k_cache, v_cache)
+    _head_dim(d, k_cache, v_cache)
     num_pages, page_size, h_kv, _ = k_cache.shape
     strides = kv_strides(k_cache)
     if kv_strides(v_cache) != strides:
@@ -512,7 +522,7 @@ def _attend_mass(q, k_cache, v_cache, block_table, mass, scale, out, ws, seq_len
     that adds the positions' weights to ``mass``."""
     _need(q, "q", torch.bfloat16)
     batch, h_q, d = q.shape
-    _head_dim(q, k_cache, v_cache)
+    _head_dim(d, k_cache, v_cache)
     kv, strides, (num_pages, page_size, h_kv, _) = _caches(k_cache, v_cache)
     _same_device(q, k_cache)
     bt, max_pages = _table(block_table, "block_table", batch, q)
@@ -671,7 +681,7 @@ def dense_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     _need(block_table, "block_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32)
     batch, h_q, d = q.shape
-    _head_dim(q, k_cache, v_cache)
+    _head_dim(d, k_cache, v_cache)
     num_pages, page_size, h_kv, _ = k_cache.shape
     strides = kv_strides(k_cache)
     if kv_strides(v_cache) != strides:
@@ -707,14 +717,14 @@ def decode(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch
     _need(k_cache, "k_cache", torch.bfloat16, contiguous=False)
     _need(v_cache, "v_cache", torch.bfloat16, contiguous=False)
     batch, h_q, d = q.shape
-    _head_dim(q, k_cache, v_cache)
+    _head_dim(d, k_cache, v_cache)
     num_pages, page_size, h_kv, _ = k_cache.shape
     r = basis.shape[1]
-    for t, n, shape in ((basis, "basis", (h_kv, r, d)),
-                        (score_cache, "score_cache", (num_pages, h_kv, page_size, r)),
-                        (k_new, "k_new", (batch, h_kv, d)), (v_new, "v_new", (batch, h_kv, d))):
-        if t is not None and (t.shape[1:] != shape[1:] or t.shape[0] < shape[0]):
-            raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
+    _rows(basis, "basis", (h_kv, r, d))
+    _rows(score_cache, "score_cache", (num_pages, h_kv, page_size, r))
+    if k_new is not None:
+        _rows(k_new, "k_new", (batch, h_kv, d))
+        _rows(v_new, "v_new", (batch, h_kv, d))
     strides = kv_strides(k_cache)
     if kv_strides(v_cache) != strides:
         raise ValueError("K and V caches must share one layout")
