@@ -1059,7 +1059,7 @@ class HostPipeline:
 
     @staticmethod
     def _no_mass(layer):
-        if layer.mass is not None:
+        if getattr(layer, "mass", None) is not None:
             raise ValueError("a HostPipeline's steps do not add to a layer's mass: build the layer "
                              "without track_mass, or call its step")
 
